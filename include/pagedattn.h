@@ -44,7 +44,13 @@
  *    bounds.  Read the word with pa_read_device_status.
  *
  * Element types: query and out are bf16.  K/V are bf16 (PA_KV_BF16, x = 8) or
- * e4m3 codes (PA_KV_FP8_E4M3, x = 16); x is 16 bytes / element size.
+ * 8-bit codes (x = 16); x is 16 bytes / element size.  The codes are e4m3 with
+ * one k_scale and one v_scale (PA_KV_FP8_E4M3), or e4m3 or int8 with a scale
+ * for each block and kv head (PA_KV_FP8_E4M3_BLOCK, PA_KV_INT8_BLOCK): k_scale
+ * and v_scale are then fp32 arrays [num_blocks, num_kv_heads], a code c of
+ * block b and kv head h standing for c * scale[b][h].  Block scales are finite
+ * and not negative; for V, one outside [2^-100, 2^100] counts as the nearer
+ * end.
  * Pointer alignment: out, query, key_cache, value_cache and workspace 16 bytes;
  * block_tables and seq_lens 4 bytes.
  * Supported shapes: head_size 64 or 128; block_size 16 or 32;
@@ -72,7 +78,9 @@ typedef enum pa_status {
 
 typedef enum pa_kv_dtype {
     PA_KV_BF16 = 0,
-    PA_KV_FP8_E4M3 = 1             /* OCP e4m3 ("fn"): bias 7, no inf, 0x7F/0xFF = NaN  */
+    PA_KV_FP8_E4M3 = 1,            /* OCP e4m3 ("fn"): bias 7, no inf, 0x7F/0xFF = NaN  */
+    PA_KV_FP8_E4M3_BLOCK = 2,      /* e4m3, a scale per (block, kv head)                */
+    PA_KV_INT8_BLOCK = 3           /* int8 (-127..127), a scale per (block, kv head)    */
 } pa_kv_dtype;
 
 /* Bits a kernel ORs into the workspace status word (never cleared by kernels). */
@@ -81,6 +89,9 @@ typedef enum pa_kv_dtype {
                                            max_seq_len's partitions: length clamped           */
 #define PA_DEV_WAIT_TIMEOUT 0x4u        /* a page copy did not land within ~2 s: output void  */
 #define PA_DEV_PREFIX_MISMATCH 0x8u     /* a declared shared prefix does not hold             */
+#define PA_DEV_BAD_QUERY_START 0x10u    /* query_start outside [0, num_tokens] or decreasing:
+                                           the sequence skipped                               */
+#define PA_DEV_POSITION_OUT_OF_RANGE 0x20u /* a position outside [0, max_position): clamped   */
 
 /* Bytes at the start of the workspace reserved for the status word. */
 #define PA_WORKSPACE_HEADER_BYTES 256
@@ -256,8 +267,9 @@ size_t pa_decode_workspace_size(int num_seqs, int num_heads, int num_kv_heads, i
  *  seq_lens     int32 [num_seqs]; 0 gives a zero output row.
  *  max_seq_len  upper bound of seq_lens, used only to plan the split.
  *  num_blocks   blocks in each cache (bounds for block ids).
- *  k_scale, v_scale  device pointers to one fp32 each; required for FP8,
- *               ignored for bf16.
+ *  k_scale, v_scale  device pointers to one fp32 each (PA_KV_FP8_E4M3), or to
+ *               fp32 [num_blocks, num_kv_heads] (block scales); required for
+ *               8-bit caches, ignored for bf16.
  *  workspace    device buffer of workspace_bytes (see above).
  *  stream       cudaStream_t to enqueue on.
  * All pointers are device pointers.  Accumulation is fp32; out is rounded
@@ -398,12 +410,89 @@ const char* pa_bm_last_error_detail(void);                     /* this thread's 
  * arrays of int64 block ids.  A dst id must not appear twice, nor as a src,
  * in one call.  Pairs with an id outside [0, num_blocks) are skipped and set
  * PA_DEV_BAD_BLOCK_ID in *status (a device word; may be NULL).  Enqueued on
- * `stream`; caches 16-byte aligned.
+ * `stream`; caches 16-byte aligned.  A cache with block scales is copied with
+ * pa_copy_blocks_ex, which takes the scale arrays and copies the blocks' scales
+ * too (they are not looked at for the other types).
  */
 pa_status pa_copy_blocks(void* key_cache, void* value_cache, int num_kv_heads, int head_size,
                          int block_size, int64_t num_blocks, pa_kv_dtype kv_dtype,
                          const int64_t* src, const int64_t* dst, int num_pairs,
                          uint32_t* status, void* stream);
+pa_status pa_copy_blocks_ex(void* key_cache, void* value_cache, float* k_scale, float* v_scale,
+                            int num_kv_heads, int head_size, int block_size, int64_t num_blocks,
+                            pa_kv_dtype kv_dtype, const int64_t* src, const int64_t* dst,
+                            int num_pairs, uint32_t* status, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Appending tokens: write new tokens' keys and values into the paged cache,
+ * and rotate keys and queries by their positions on the way.
+ *
+ * Row r of key / value is one token.  Sequence s owns the rows
+ * query_start[s] .. query_start[s + 1] - 1, which are its last n_s tokens:
+ * seq_lens[s] counts them already (as pa_bm_export gives it after
+ * pa_bm_append_tokens), so row query_start[s] + i is the token with index
+ * t = seq_lens[s] - n_s + i and goes to slot t mod block_size of block
+ * block_tables[s][t / block_size].  A sequence may have no rows.  Rows outside
+ * [query_start[0], query_start[num_seqs]) -- padding -- are neither read nor
+ * written.  query_start NULL: every sequence has one row (num_tokens ==
+ * num_seqs), as in a decode step.  No two sequences of a call may append into
+ * the same block (copy on write sees to that).
+ *
+ * Rotation (opts->cos_sin): with p a token's position and R = rotary_dim, the
+ * pairs (a, b) of elements (d, d + R/2), or (2d, 2d + 1) when interleaved,
+ * d < R/2, become (a cos - b sin, a sin + b cos) with cos = cos_sin[p][d] and
+ * sin = cos_sin[p][R/2 + d]; products and sums are each rounded in fp32.
+ * Elements from R on are left as they are.  Keys and, if given, queries
+ * (query -> query_out) are rotated, values are not.
+ *
+ * What is stored: bf16 (round to nearest even); or e4m3 codes of x / k_scale
+ * (x / v_scale for values), saturating; or, with block scales, codes of
+ * x / scale[block][kv head], where the call also sets the scale: the smallest
+ * power of two 2^e, -100 <= e <= 100, with |x| <= M 2^e over the call's tokens
+ * in the block (M = 448 for e4m3, 127 for int8; infinities and NaNs do not
+ * count), or the scale that the block has already if that is larger and the
+ * run does not begin the block.  When a block's scale grows, the codes of its
+ * earlier tokens are rounded to the new scale.  A run that begins a block
+ * (t mod block_size == 0) ignores the block's old scale, so blocks need no
+ * clearing when they are reused.  Infinities saturate; a NaN becomes the e4m3
+ * NaN, or int8 0.  Slots that the call's tokens do not fill keep their contents.
+ *
+ * Device data is checked as everywhere: a bad query_start or length skips the
+ * sequence (PA_DEV_BAD_QUERY_START, PA_DEV_SEQ_LEN_OUT_OF_RANGE), a bad block
+ * id skips the block, a position outside [0, max_position) is clamped; each
+ * sets its bit in *status (a device word; may be NULL), and nothing is read or
+ * written out of bounds.
+ *
+ *  key_stride, value_stride, query_stride, query_out_stride: elements from one
+ *      token's row to the next, a multiple of 8; 0 = dense.  Heads are dense.
+ *  cos_sin: fp32 [max_position, rotary_dim], or NULL for no rotation;
+ *      rotary_dim a multiple of 16, at most head_size; 16-byte aligned.
+ *  interleaved: non-zero pairs (2d, 2d + 1).
+ *  positions: int32 [num_tokens], or NULL for the tokens' indices t.
+ *  query, query_out: bf16 [num_tokens, num_heads, head_size]; they may be the
+ *      same memory (with the same stride).  Both NULL: keys only.
+ * key, value, query, query_out and the caches are 16-byte aligned.  Enqueued
+ * on `stream`; allocates nothing and never synchronises.
+ * ------------------------------------------------------------------------ */
+typedef struct pa_append_options {
+    int64_t key_stride, value_stride;
+    const float* cos_sin;
+    int max_position;
+    int rotary_dim;
+    int interleaved;
+    int num_heads;
+    const int32_t* positions;
+    const void* query;
+    void* query_out;
+    int64_t query_stride, query_out_stride;
+} pa_append_options;
+
+pa_status pa_append_kv(void* key_cache, void* value_cache, const void* key, const void* value,
+                       int num_tokens, int num_seqs, int num_kv_heads, int head_size,
+                       const int32_t* block_tables, int max_blocks_per_seq,
+                       const int32_t* seq_lens, const int32_t* query_start, int block_size,
+                       int64_t num_blocks, pa_kv_dtype kv_dtype, float* k_scale, float* v_scale,
+                       uint32_t* status, void* stream, const pa_append_options* opts);
 
 #ifdef __cplusplus
 }

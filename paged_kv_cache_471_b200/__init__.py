@@ -12,7 +12,9 @@ v_scale), with the split-KV temporaries folded into one optional workspace.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 import threading
 
@@ -28,18 +30,24 @@ PA_ERR_OUT_OF_BLOCKS = 5
 
 PA_KV_BF16 = 0
 PA_KV_FP8_E4M3 = 1
+PA_KV_FP8_E4M3_BLOCK = 2
+PA_KV_INT8_BLOCK = 3
 
 PA_DEV_BAD_BLOCK_ID = 0x1
 PA_DEV_SEQ_LEN_OUT_OF_RANGE = 0x2
 PA_DEV_WAIT_TIMEOUT = 0x4
 PA_DEV_PREFIX_MISMATCH = 0x8
+PA_DEV_BAD_QUERY_START = 0x10
+PA_DEV_POSITION_OUT_OF_RANGE = 0x20
 
 WORKSPACE_HEADER_BYTES = 256
 WORKSPACE_MERGE_COUNT_BYTES = 4096  # after the header when the plan needs more
 NOALLOC_SCRATCH_BYTES = 16 << 20
 
 _KV = {"bf16": PA_KV_BF16, "auto": PA_KV_BF16, "fp8": PA_KV_FP8_E4M3, "fp8_e4m3": PA_KV_FP8_E4M3,
-       PA_KV_BF16: PA_KV_BF16, PA_KV_FP8_E4M3: PA_KV_FP8_E4M3}
+       "fp8_e4m3_block": PA_KV_FP8_E4M3_BLOCK, "int8_block": PA_KV_INT8_BLOCK,
+       PA_KV_BF16: PA_KV_BF16, PA_KV_FP8_E4M3: PA_KV_FP8_E4M3,
+       PA_KV_FP8_E4M3_BLOCK: PA_KV_FP8_E4M3_BLOCK, PA_KV_INT8_BLOCK: PA_KV_INT8_BLOCK}
 
 
 class PagedAttentionError(RuntimeError):
@@ -54,6 +62,15 @@ class Options(ctypes.Structure):
                 ("alibi_slopes", ctypes.c_void_p), ("fp8_compute", ctypes.c_int),
                 ("test_stall_copies", ctypes.c_int), ("schedule", ctypes.c_int),
                 ("mha_cuda_cores", ctypes.c_int)]
+
+
+class AppendOptions(ctypes.Structure):
+    _fields_ = [("key_stride", ctypes.c_int64), ("value_stride", ctypes.c_int64),
+                ("cos_sin", ctypes.c_void_p), ("max_position", ctypes.c_int),
+                ("rotary_dim", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("num_heads", ctypes.c_int), ("positions", ctypes.c_void_p),
+                ("query", ctypes.c_void_p), ("query_out", ctypes.c_void_p),
+                ("query_stride", ctypes.c_int64), ("query_out_stride", ctypes.c_int64)]
 
 
 class Plan(ctypes.Structure):
@@ -125,6 +142,11 @@ def _bind(lib):
     lib.pa_bm_last_error_detail.restype = ctypes.c_char_p
     lib.pa_copy_blocks.argtypes = [_P, _P, _I, _I, _I, I64, _I, _P, _P, _I, _P, _P]
     lib.pa_copy_blocks.restype = _I
+    lib.pa_copy_blocks_ex.argtypes = [_P, _P, _P, _P, _I, _I, _I, I64, _I, _P, _P, _I, _P, _P]
+    lib.pa_copy_blocks_ex.restype = _I
+    lib.pa_append_kv.argtypes = [_P, _P, _P, _P, _I, _I, _I, _I, _P, _I, _P, _P, _I, I64, _I, _P,
+                                 _P, _P, _P, ctypes.POINTER(AppendOptions)]
+    lib.pa_append_kv.restype = _I
     return lib
 
 
@@ -184,6 +206,12 @@ def plan(num_seqs, num_heads, num_kv_heads, head_size, block_size, max_seq_len, 
     return p.as_dict()
 
 
+@functools.lru_cache(maxsize=4096)
+def _workspace_size(device, *args, **kw):
+    """workspace_size for the current device (number `device`)."""
+    return workspace_size(*args, **kw)
+
+
 def workspace_size(num_seqs, num_heads, num_kv_heads, head_size, block_size, max_seq_len,
                    kv_dtype="bf16", partition_pages=0, num_sms=0, shared_prefix_blocks=0,
                    fp8_compute=False, schedule="auto", stages=0) -> int:
@@ -197,19 +225,55 @@ def workspace_size(num_seqs, num_heads, num_kv_heads, head_size, block_size, max
 
 
 _ws_cache = {}
+_status_words = {}
 
 
-def workspace(nbytes: int, device):
-    """A zeroed workspace of at least nbytes on `device`, reused across calls
-    (its status word is sticky; see read_status)."""
+def workspace(nbytes: int, device, stream=None):
+    """A zeroed workspace of at least nbytes on `device` for calls on `stream`
+    (default: the current one), reused by the calls on that stream (its status
+    word is sticky; see read_status).  Calls on different streams may overlap,
+    so each stream has its own.  While the stream is being captured into a
+    graph, the workspace is a new one that belongs to the graph alone and is
+    zeroed by each replay."""
     import torch
     dev = torch.device(device)
-    key = (dev.type, dev.index)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    nbytes = max(nbytes, WORKSPACE_HEADER_BYTES)
+    if torch.cuda.is_current_stream_capturing():
+        with torch.cuda.stream(stream):
+            return torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+    key = (dev.type, dev.index, stream.cuda_stream)
     ws = _ws_cache.get(key)
     if ws is None or ws.numel() < nbytes:
-        ws = torch.zeros(max(nbytes, WORKSPACE_HEADER_BYTES), dtype=torch.uint8, device=dev)
-        _ws_cache[key] = ws
+        with torch.cuda.stream(stream):  # zeroed, and later freed, in that stream's order
+            new = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+            if ws is not None:  # keep the status bits
+                new[:4] = ws[:4]
+        ws = _ws_cache[key] = new
     return ws
+
+
+def _status_word(dev):
+    """The device word that append_kv reports to by default; read_status reads
+    it with the workspaces'.  None while capturing if no call made it before."""
+    import torch
+    word = _status_words.get(dev.index)
+    if word is None:
+        if torch.cuda.is_current_stream_capturing():
+            return None
+        word = torch.zeros(4, dtype=torch.int32, device=dev)
+        torch.cuda.synchronize(dev)  # once per device: zeroed before any stream's call
+        _status_words[dev.index] = word
+    return word
+
+
+def _on_device(dev):
+    """The library launches on the current device: make it `dev`."""
+    import torch
+    if torch.cuda.current_device() == dev.index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
 
 
 def _ptr(t, name, dtypes=None, device=None):
@@ -227,6 +291,29 @@ def _ptr(t, name, dtypes=None, device=None):
     return t.data_ptr()
 
 
+def _kv_types(code):
+    import torch
+    if code == PA_KV_BF16:
+        return (torch.bfloat16,)
+    if code == PA_KV_INT8_BLOCK:
+        return (torch.int8, torch.uint8)
+    return (torch.uint8, torch.float8_e4m3fn)
+
+
+def _scale_ptrs(code, k_scale, v_scale, num_blocks, num_kv_heads, dev):
+    """Pointers to the scales of an 8-bit cache (None, None for bf16)."""
+    import torch
+    if code == PA_KV_BF16:
+        return None, None
+    ptrs = (_ptr(k_scale, "k_scale", (torch.float32,), dev),
+            _ptr(v_scale, "v_scale", (torch.float32,), dev))
+    if code != PA_KV_FP8_E4M3:
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t.shape != (num_blocks, num_kv_heads):
+                raise ValueError(f"{name} must be [num_blocks, num_kv_heads] for block scales")
+    return ptrs
+
+
 def decode(out, query, key_cache, value_cache, num_kv_heads: int, scale: float, block_tables,
            seq_lens, block_size: int, max_seq_len: int, kv_dtype="bf16", k_scale=None,
            v_scale=None, workspace_tensor=None, partition_pages: int = 0, stream=None,
@@ -238,21 +325,24 @@ def decode(out, query, key_cache, value_cache, num_kv_heads: int, scale: float, 
     key_cache: [num_blocks, num_kv_heads, head_size/x, block_size, x];
     value_cache: [num_blocks, num_kv_heads, head_size, block_size]; bf16, or
     uint8 / float8_e4m3fn holding e4m3 codes when kv_dtype is "fp8_e4m3"
-    (then k_scale / v_scale are 1-element fp32 CUDA tensors).
+    (then k_scale / v_scale are 1-element fp32 CUDA tensors), or e4m3 or int8
+    codes when it is "fp8_e4m3_block" or "int8_block" (then k_scale / v_scale
+    are fp32 [num_blocks, num_kv_heads], a scale for each block and kv head;
+    no fp8_compute and no dynamic schedule).
 
     The keyword options are those of pa_options in include/pagedattn.h:
     partition_pages, stages, shared_prefix_blocks, alibi_slopes ([num_heads]
     fp32), fp8_compute, test_stall_copies, schedule ("auto",
     "partitioned", "balanced" or "dynamic"), mha_cuda_cores and num_sms (plan
     as if the GPU had that many SMs; 0 = the device's count).  workspace_tensor
-    defaults to a cached zeroed buffer per device; stream defaults to the
-    current stream.
+    defaults to a cached zeroed buffer per device and stream; stream defaults
+    to the current stream.
     """
     import torch
     code = kv_dtype_code(kv_dtype)
     dev = query.device
     S, Hq, D = query.shape
-    kv_types = (torch.bfloat16,) if code == PA_KV_BF16 else (torch.uint8, torch.float8_e4m3fn)
+    kv_types = _kv_types(code)
     args_ptrs = [
         _ptr(out, "out", (torch.bfloat16,), dev),
         _ptr(query, "query", (torch.bfloat16,), dev),
@@ -273,10 +363,7 @@ def decode(out, query, key_cache, value_cache, num_kv_heads: int, scale: float, 
     sl = _ptr(seq_lens, "seq_lens", (torch.int32,), dev)
     if block_tables.dim() != 2 or block_tables.shape[0] != S or seq_lens.shape != (S,):
         raise ValueError("block_tables must be [num_seqs, max_blocks] and seq_lens [num_seqs]")
-    ks = vs = None
-    if code == PA_KV_FP8_E4M3:
-        ks = _ptr(k_scale, "k_scale", (torch.float32,), dev)
-        vs = _ptr(v_scale, "v_scale", (torch.float32,), dev)
+    ks, vs = _scale_ptrs(code, k_scale, v_scale, num_blocks, num_kv_heads, dev)
     alibi = None
     if alibi_slopes is not None:
         if alibi_slopes.shape != (Hq,):
@@ -285,13 +372,14 @@ def decode(out, query, key_cache, value_cache, num_kv_heads: int, scale: float, 
     st = stream if stream is not None else torch.cuda.current_stream(dev)
     # The library plans for, and launches on, the current device: make it the
     # tensors' device for the call.
-    with torch.cuda.device(dev):
+    with _on_device(dev):
         if workspace_tensor is None:  # (a given one is size-checked by the library)
-            need = workspace_size(S, Hq, num_kv_heads, D, block_size, max_seq_len, code,
-                                  partition_pages, shared_prefix_blocks=shared_prefix_blocks,
-                                  fp8_compute=fp8_compute and code == PA_KV_FP8_E4M3,
-                                  schedule=schedule, stages=stages, num_sms=num_sms)
-            workspace_tensor = workspace(need, dev)
+            need = _workspace_size(dev.index, S, Hq, num_kv_heads, D, block_size, max_seq_len,
+                                   code, partition_pages,
+                                   shared_prefix_blocks=shared_prefix_blocks,
+                                   fp8_compute=bool(fp8_compute) and code == PA_KV_FP8_E4M3,
+                                   schedule=schedule, stages=stages, num_sms=num_sms)
+            workspace_tensor = workspace(need, dev, st)
         ws = _ptr(workspace_tensor, "workspace", None, dev)
         rc = lib().pa_decode_ex(*args_ptrs, S, Hq, int(num_kv_heads), D, float(scale), bt,
                                 block_tables.shape[1], sl, int(block_size), int(max_seq_len),
@@ -316,11 +404,8 @@ def decode_noalloc(out, query, key_cache, value_cache, num_kv_heads: int, scale:
     code = kv_dtype_code(kv_dtype)
     dev = query.device
     S, Hq, D = query.shape
-    kv_types = (torch.bfloat16,) if code == PA_KV_BF16 else (torch.uint8, torch.float8_e4m3fn)
-    ks = vs = None
-    if code == PA_KV_FP8_E4M3:
-        ks = _ptr(k_scale, "k_scale", (torch.float32,), dev)
-        vs = _ptr(v_scale, "v_scale", (torch.float32,), dev)
+    kv_types = _kv_types(code)
+    ks, vs = _scale_ptrs(code, k_scale, v_scale, key_cache.shape[0], num_kv_heads, dev)
     st = stream if stream is not None else torch.cuda.current_stream(dev)
     ptrs = (_ptr(out, "out", (torch.bfloat16,), dev), _ptr(query, "query", (torch.bfloat16,), dev),
             _ptr(key_cache, "key_cache", kv_types, dev),
@@ -336,18 +421,31 @@ def decode_noalloc(out, query, key_cache, value_cache, num_kv_heads: int, scale:
 
 
 def read_status(workspace_tensor=None, device=None, clear=False, stream=None) -> int:
-    """The sticky PA_DEV_* bits kernels set in a workspace (synchronises)."""
+    """The sticky PA_DEV_* bits kernels set (synchronises): those of a
+    workspace, or, without one, those of every call on the device that was
+    given none."""
     import torch
-    if workspace_tensor is None:
-        dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
-        workspace_tensor = workspace(WORKSPACE_HEADER_BYTES, dev)
-    st = stream if stream is not None else torch.cuda.current_stream(workspace_tensor.device)
-    flags = ctypes.c_uint32(0)
-    with torch.cuda.device(workspace_tensor.device):
-        rc = lib().pa_read_device_status(ctypes.c_void_p(workspace_tensor.data_ptr()),
-                                         ctypes.byref(flags), int(bool(clear)), st.cuda_stream)
-    _check(rc)
-    return int(flags.value)
+    if workspace_tensor is not None:
+        dev, words = workspace_tensor.device, [workspace_tensor]
+    else:
+        dev = torch.device(device) if device is not None else torch.device("cuda")
+        if dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        words = [ws for key, ws in _ws_cache.items() if key[1] == dev.index]
+        words += [w for index, w in _status_words.items() if index == dev.index]
+        if words:  # calls of other streams may still be running
+            torch.cuda.synchronize(dev)
+    st = stream if stream is not None else torch.cuda.current_stream(dev)
+    bits = 0
+    with torch.cuda.device(dev):
+        for w in words:
+            flags = ctypes.c_uint32(0)
+            _check(lib().pa_read_device_status(ctypes.c_void_p(w.data_ptr()), ctypes.byref(flags),
+                                               int(bool(clear)), st.cuda_stream))
+            bits |= int(flags.value)
+        if clear and workspace_tensor is None and words:
+            torch.cuda.synchronize(dev)  # cleared before calls on other streams follow
+    return bits
 
 
 def version() -> int:
@@ -426,23 +524,137 @@ class BlockManager:
         return int(lib().pa_bm_refcount(self._h, int(block)))
 
 
-def copy_blocks(key_cache, value_cache, src, dst, kv_dtype="bf16", status=None, stream=None):
+def copy_blocks(key_cache, value_cache, src, dst, kv_dtype="bf16", status=None, stream=None,
+                k_scale=None, v_scale=None):
     """Copy whole blocks (all kv heads, K and V): block dst[i] <- block src[i].
-    src / dst: int64 CUDA tensors of block ids."""
+    src / dst: int64 CUDA tensors of block ids.  A cache with block scales
+    needs k_scale and v_scale ([num_blocks, num_kv_heads]), whose rows are
+    copied with the blocks."""
     import torch
     code = kv_dtype_code(kv_dtype)
     dev = key_cache.device
-    kv_types = (torch.bfloat16,) if code == PA_KV_BF16 else (torch.uint8, torch.float8_e4m3fn)
+    kv_types = _kv_types(code)
     n = int(src.numel())
     if int(dst.numel()) != n:
         raise ValueError("src and dst must have the same length")
     Hk, D = value_cache.shape[1], value_cache.shape[2]
     st = stream if stream is not None else torch.cuda.current_stream(dev)
+    ks = vs = None
+    if code in (PA_KV_FP8_E4M3_BLOCK, PA_KV_INT8_BLOCK):
+        ks, vs = _scale_ptrs(code, k_scale, v_scale, key_cache.shape[0], Hk, dev)
     args = (_ptr(key_cache, "key_cache", kv_types, dev),
-            _ptr(value_cache, "value_cache", kv_types, dev),
+            _ptr(value_cache, "value_cache", kv_types, dev), ks, vs,
             int(Hk), int(D), int(value_cache.shape[3]), int(key_cache.shape[0]), code,
             _ptr(src, "src", (torch.int64,), dev), _ptr(dst, "dst", (torch.int64,), dev), n,
             None if status is None else _ptr(status, "status", None, dev), st.cuda_stream)
     with torch.cuda.device(dev):
-        rc = lib().pa_copy_blocks(*args)
+        rc = lib().pa_copy_blocks_ex(*args)
     _bm_check(rc)
+
+
+# ------------------------------------------------------------- appending tokens
+def _rows(t, name, heads, head_size, dev):
+    """Pointer and row stride of a bf16 [tokens, heads, head_size] tensor whose
+    heads are dense (a view of a wider projection's output will do)."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected torch.bfloat16")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_size:
+        raise ValueError(f"{name} must be [num_tokens, {heads}, {head_size}]")
+    n, stride = t.shape[0], t.stride()
+    if n and (stride[2] != 1 or (heads > 1 and stride[1] != head_size)):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    if n > 1 and stride[0] < heads * head_size:
+        raise ValueError(f"{name}: its rows overlap")
+    return t.data_ptr(), stride[0] if n > 1 else 0
+
+
+def append_kv(key_cache, value_cache, key, value, block_tables, seq_lens, block_size: int,
+              kv_dtype="bf16", k_scale=None, v_scale=None, *, query_start=None, cos_sin=None,
+              interleaved: bool = False, positions=None, query=None, query_out=None, status=None,
+              stream=None):
+    """Write new tokens' keys and values into a paged cache, keys (and queries)
+    rotated by their positions on the way.
+
+    key, value: bf16 [num_tokens, num_kv_heads, head_size]; rows may be strided
+    (views of one projection's output).  Rows query_start[s] ..
+    query_start[s + 1] - 1 (int32 [num_seqs + 1]) are the last tokens of
+    sequence s, whose length with them is seq_lens[s]; None: one row per
+    sequence, as in a decode step.  Rows that no sequence owns (padding) are
+    left alone.
+
+    cos_sin: fp32 [max_position, rotary_dim], a row holding the cosines, then
+    the sines of its position's rotary_dim / 2 angles; pairs are (d, d +
+    rotary_dim / 2), or (2d, 2d + 1) with interleaved.  positions: int32
+    [num_tokens] (default: a token's index in its sequence).  query is rotated
+    into query_out (default: in place).
+
+    kv_dtype and the scales are those of decode; with block scales, k_scale and
+    v_scale are updated: see pa_append_kv in include/pagedattn.h.  status: an
+    int32 / uint32 CUDA word for the PA_DEV_* bits (default: one that
+    read_status reads).  Returns query_out (None without a query).
+    """
+    import torch
+    code = kv_dtype_code(kv_dtype)
+    dev = key_cache.device
+    kv_types = _kv_types(code)
+    kc = _ptr(key_cache, "key_cache", kv_types, dev)
+    vc = _ptr(value_cache, "value_cache", kv_types, dev)
+    if key_cache.dim() != 5 or value_cache.dim() != 4:
+        raise ValueError("key_cache must be 5-D and value_cache 4-D")
+    num_blocks, Hk, D = value_cache.shape[:3]
+    if value_cache.shape[3] != block_size \
+            or key_cache.shape != (num_blocks, Hk, D * key_cache.element_size() // 16, block_size,
+                                   16 // key_cache.element_size()):
+        raise ValueError("cache shapes do not match each other / block_size")
+    k, k_stride = _rows(key, "key", Hk, D, dev)
+    v, v_stride = _rows(value, "value", Hk, D, dev)
+    T, S = key.shape[0], seq_lens.shape[0]
+    bt = _ptr(block_tables, "block_tables", (torch.int32,), dev)
+    sl = _ptr(seq_lens, "seq_lens", (torch.int32,), dev)
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or seq_lens.dim() != 1:
+        raise ValueError("block_tables must be [num_seqs, max_blocks] and seq_lens [num_seqs]")
+    qs = None
+    if query_start is not None:
+        qs = _ptr(query_start, "query_start", (torch.int32,), dev)
+        if query_start.shape != (S + 1,):
+            raise ValueError("query_start must be [num_seqs + 1]")
+    if value.shape[0] != T or (qs is None and T != S):
+        raise ValueError("key and value need a row per token (per sequence without query_start)")
+    ks, vs = _scale_ptrs(code, k_scale, v_scale, num_blocks, Hk, dev)
+    o = AppendOptions(key_stride=k_stride, value_stride=v_stride)
+    if cos_sin is not None:
+        o.cos_sin = _ptr(cos_sin, "cos_sin", (torch.float32,), dev)
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be [max_position, rotary_dim]")
+        o.max_position, o.rotary_dim = cos_sin.shape
+        o.interleaved = int(bool(interleaved))
+        if positions is not None:
+            o.positions = _ptr(positions, "positions", (torch.int32,), dev)
+            if positions.shape != (T,):
+                raise ValueError("positions must be [num_tokens]")
+        if query is not None:
+            if query_out is None:
+                query_out = query
+            o.num_heads = Hq = query.shape[1]
+            o.query, o.query_stride = _rows(query, "query", Hq, D, dev)
+            o.query_out, o.query_out_stride = _rows(query_out, "query_out", Hq, D, dev)
+            if query.shape[0] != T or query_out.shape[0] != T:
+                raise ValueError("query and query_out need a row per token")
+        elif query_out is not None:
+            raise ValueError("query_out needs query")
+    elif positions is not None or query is not None or query_out is not None or interleaved:
+        raise ValueError("positions, query, query_out and interleaved need cos_sin")
+    st = stream if stream is not None else torch.cuda.current_stream(dev)
+    with _on_device(dev):
+        word = _status_word(dev) if status is None else status
+        rc = lib().pa_append_kv(kc, vc, k, v, T, S, Hk, D, bt, block_tables.shape[1], sl, qs,
+                                int(block_size), num_blocks, code, ks, vs,
+                                None if word is None else _ptr(word, "status", None, dev),
+                                st.cuda_stream, ctypes.byref(o))
+    _check(rc)
+    return query_out

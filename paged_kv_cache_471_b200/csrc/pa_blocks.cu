@@ -232,10 +232,12 @@ constexpr int kCopyUnroll = 4;
 
 // One CTA per (pair, cache half, slice): copies `slice` 16-byte words of one
 // block's K (blockIdx.y == 0) or V (== 1) bytes from block src[i] to dst[i].
-// Pairs with an id outside [0, num_blocks) are skipped and flagged.
+// Pairs with an id outside [0, num_blocks) are skipped and flagged.  With
+// block scales, a block's first slice brings them along.
 __global__ void __launch_bounds__(kCopyThreads) pa_copy_blocks_kernel(
     uint8_t* key_cache, uint8_t* value_cache, long long block_words, long long slice_words,
-    const int64_t* src, const int64_t* dst, long long num_blocks, uint32_t* status) {
+    const int64_t* src, const int64_t* dst, long long num_blocks, uint32_t* status,
+    float* k_scale, float* v_scale, int num_kv_heads) {
     const long long i = blockIdx.x;
     const int64_t a = src[i];
     const int64_t b = dst[i];
@@ -243,6 +245,11 @@ __global__ void __launch_bounds__(kCopyThreads) pa_copy_blocks_kernel(
         if (threadIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && status)
             atomicOr(status, PA_DEV_BAD_BLOCK_ID);
         return;
+    }
+    float* scale = blockIdx.y == 0 ? k_scale : v_scale;
+    if (scale && blockIdx.z == 0) {  // the block's scales, one per kv head
+        for (int h = threadIdx.x; h < num_kv_heads; h += kCopyThreads)
+            scale[b * num_kv_heads + h] = scale[a * num_kv_heads + h];
     }
     uint8_t* base = blockIdx.y == 0 ? key_cache : value_cache;
     const uint4* from = reinterpret_cast<const uint4*>(base) + a * block_words;
@@ -266,10 +273,11 @@ __global__ void __launch_bounds__(kCopyThreads) pa_copy_blocks_kernel(
 
 }  // namespace
 
-extern "C" pa_status pa_copy_blocks(void* key_cache, void* value_cache, int num_kv_heads,
-                                    int head_size, int block_size, int64_t num_blocks,
-                                    pa_kv_dtype kv_dtype, const int64_t* src, const int64_t* dst,
-                                    int num_pairs, uint32_t* status, void* stream) {
+extern "C" pa_status pa_copy_blocks_ex(void* key_cache, void* value_cache, float* k_scale,
+                                       float* v_scale, int num_kv_heads, int head_size,
+                                       int block_size, int64_t num_blocks, pa_kv_dtype kv_dtype,
+                                       const int64_t* src, const int64_t* dst, int num_pairs,
+                                       uint32_t* status, void* stream) {
     g_bm_detail[0] = 0;
     if (num_pairs < 0) return bm_fail(PA_ERR_INVALID_ARG, "num_pairs < 0");
     if (num_pairs == 0) return PA_OK;
@@ -283,9 +291,16 @@ extern "C" pa_status pa_copy_blocks(void* key_cache, void* value_cache, int num_
         return bm_fail(PA_ERR_INVALID_ARG, "status must be 4-byte aligned");
     if (num_kv_heads < 1 || head_size < 1 || block_size < 1 || num_blocks < 1)
         return bm_fail(PA_ERR_INVALID_ARG, "sizes must be positive");
-    if (kv_dtype != PA_KV_BF16 && kv_dtype != PA_KV_FP8_E4M3)
+    const bool block_scales =
+        kv_dtype == PA_KV_FP8_E4M3_BLOCK || kv_dtype == PA_KV_INT8_BLOCK;
+    if (kv_dtype != PA_KV_BF16 && kv_dtype != PA_KV_FP8_E4M3 && !block_scales)
         return bm_fail(PA_ERR_UNSUPPORTED, "kv_dtype");
-    const long long elem = kv_dtype == PA_KV_FP8_E4M3 ? 1 : 2;
+    if (block_scales && (!k_scale || !v_scale))
+        return bm_fail(PA_ERR_INVALID_ARG,
+                       "a cache with block scales needs k_scale and v_scale (pa_copy_blocks_ex)");
+    if ((reinterpret_cast<uintptr_t>(k_scale) | reinterpret_cast<uintptr_t>(v_scale)) % 4)
+        return bm_fail(PA_ERR_INVALID_ARG, "k_scale / v_scale must be 4-byte aligned");
+    const long long elem = kv_dtype == PA_KV_BF16 ? 2 : 1;
     const long long block_bytes = static_cast<long long>(num_kv_heads) * head_size * block_size * elem;
     if (block_bytes % 16) return bm_fail(PA_ERR_UNSUPPORTED, "block bytes not a multiple of 16");
     const long long words = block_bytes / 16;
@@ -296,8 +311,17 @@ extern "C" pa_status pa_copy_blocks(void* key_cache, void* value_cache, int num_
     dim3 grid(static_cast<unsigned>(num_pairs), 2, static_cast<unsigned>(slices));
     pa_copy_blocks_kernel<<<grid, kCopyThreads, 0, static_cast<cudaStream_t>(stream)>>>(
         static_cast<uint8_t*>(key_cache), static_cast<uint8_t*>(value_cache), words, slice, src,
-        dst, num_blocks, status);
+        dst, num_blocks, status, block_scales ? k_scale : nullptr,
+        block_scales ? v_scale : nullptr, num_kv_heads);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return bm_fail(PA_ERR_CUDA, cudaGetErrorString(e));
     return PA_OK;
+}
+
+extern "C" pa_status pa_copy_blocks(void* key_cache, void* value_cache, int num_kv_heads,
+                                    int head_size, int block_size, int64_t num_blocks,
+                                    pa_kv_dtype kv_dtype, const int64_t* src, const int64_t* dst,
+                                    int num_pairs, uint32_t* status, void* stream) {
+    return pa_copy_blocks_ex(key_cache, value_cache, nullptr, nullptr, num_kv_heads, head_size,
+                             block_size, num_blocks, kv_dtype, src, dst, num_pairs, status, stream);
 }

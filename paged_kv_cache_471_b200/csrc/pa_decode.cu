@@ -12,15 +12,26 @@
 
 #include "pa_decode_dynamic.cuh"
 #include "pa_decode_kernels.cuh"
+#include "pa_launch.cuh"
 #include "pagedattn.h"
 
 namespace {
 
+using pa::aligned;
+using pa::block_scales;
+using pa::device_sms;
+using pa::elem_bytes;
+using pa::ensure_smem;
+using pa::fail;
+using pa::kMaxDevices;
+using pa::kMaxSmemPerCta;
+using pa::kStaticSmemReserve;
+using pa::launch_decode;
+using pa::launch_pdl;
+
 constexpr int kVersion = 10000;  // 1.0.0
 constexpr size_t kSmemPerSm = 228 * 1024;
 constexpr size_t kSmemReservedPerCta = 1024;
-constexpr size_t kMaxSmemPerCta = 227 * 1024;  // opt-in limit of sm_100
-constexpr size_t kStaticSmemReserve = 256;      // the kernel's own __shared__ variables
 constexpr int kMinPartitionPages = 16;
 constexpr int kMaxRankedSeqs = 256;  // batches ranked by length on the device
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;   // a page copy's wait bound
@@ -50,19 +61,20 @@ constexpr int kMaxShortStages = 4;
 constexpr size_t kShortStagesSmem = 96 * 1024;  // keep >= 2 CTAs per SM
 constexpr long long kMaxCtasPerSm = 3;
 constexpr int kMaxForcedStages = 16;
-constexpr int kMaxDevices = 64;
 constexpr long long kMaxDynSlots = 64;  // partial slots per row and unit kind (dynamic schedule)
 
 thread_local char g_detail[256] = "";
 
-pa_status fail(pa_status st, const char* fmt, const char* what) {
+}  // namespace
+
+pa_status pa::fail(pa_status st, const char* fmt, const char* what) {
     std::snprintf(g_detail, sizeof g_detail, fmt, what);
     return st;
 }
 
-bool aligned(const void* ptr, size_t a) { return (reinterpret_cast<uintptr_t>(ptr) % a) == 0; }
+void pa::clear_detail() { g_detail[0] = 0; }
 
-int elem_bytes(pa_kv_dtype t) { return t == PA_KV_FP8_E4M3 ? 1 : 2; }
+namespace {
 
 pa_status check_sizes(int num_seqs, int num_heads, int num_kv_heads, int head_size,
                       int block_size, int max_seq_len, pa_kv_dtype kv_dtype) {
@@ -77,29 +89,10 @@ pa_status check_sizes(int num_seqs, int num_heads, int num_kv_heads, int head_si
         return fail(PA_ERR_UNSUPPORTED, "%s", "head_size must be 64 or 128");
     if (block_size != 16 && block_size != 32)
         return fail(PA_ERR_UNSUPPORTED, "%s", "block_size must be 16 or 32");
-    if (kv_dtype != PA_KV_BF16 && kv_dtype != PA_KV_FP8_E4M3)
+    if (kv_dtype != PA_KV_BF16 && kv_dtype != PA_KV_FP8_E4M3 && !block_scales(kv_dtype))
         return fail(PA_ERR_UNSUPPORTED, "%s", "kv_dtype");
     if (max_seq_len < 0) return fail(PA_ERR_INVALID_ARG, "%s", "max_seq_len < 0");
     return PA_OK;
-}
-
-int device_sms(int* out) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return -1;
-    static std::atomic<int> cache[kMaxDevices];
-    if (dev >= 0 && dev < kMaxDevices) {
-        int v = cache[dev].load(std::memory_order_relaxed);
-        if (v > 0) {
-            *out = v;
-            return 0;
-        }
-    }
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-        return -1;
-    if (dev >= 0 && dev < kMaxDevices) cache[dev].store(n, std::memory_order_relaxed);
-    *out = n;
-    return 0;
 }
 
 size_t merge_bytes(int head_size, int group, int warps) {
@@ -134,11 +127,13 @@ pa_status plan(pa_plan* pl, int num_seqs, int num_heads, int num_kv_heads, int h
     if (schedule != PA_SCHEDULE_AUTO && schedule != PA_SCHEDULE_BALANCED &&
         schedule != PA_SCHEDULE_PARTITIONED && schedule != PA_SCHEDULE_DYNAMIC)
         return fail(PA_ERR_INVALID_ARG, "%s", "opts->schedule");
+    if (schedule == PA_SCHEDULE_DYNAMIC && block_scales(kv_dtype))
+        return fail(PA_ERR_UNSUPPORTED, "%s", "the dynamic schedule takes no block scales");
     const bool f8mma = opts && opts->fp8_compute && kv_dtype == PA_KV_FP8_E4M3;
-    // A stage holds a K and a V page; small pages (16-token e4m3 pages, and
+    // A stage holds a K and a V page; small pages (16-token 8-bit pages, and
     // 16-token bf16 pages of head size 64) go in pairs (pa_decode_kernels.cuh,
     // pair_pages).
-    const bool pair = block_size == 16 && (kv_dtype == PA_KV_FP8_E4M3 || head_size == 64);
+    const bool pair = block_size == 16 && (elem_bytes(kv_dtype) == 1 || head_size == 64);
     const size_t stage = 2ull * head_size * block_size * elem_bytes(kv_dtype) * (pair ? 2 : 1);
     const int W = pa::decode_warps(static_cast<long long>(stage));
     int ns = kDefaultStages;
@@ -467,68 +462,10 @@ pa_status plan(pa_plan* pl, int num_seqs, int num_heads, int num_kv_heads, int h
     return PA_OK;
 }
 
-// Raise the kernel's dynamic shared-memory limit once per device.  `done` is
-// owned by the caller's template instantiation, so every kernel variant keeps
-// its own flags.
-template <typename K>
-cudaError_t ensure_smem(K kernel, std::atomic<int>* done) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const bool cached = dev >= 0 && dev < kMaxDevices;
-    if (cached && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
-    // The opt-in limit covers static and dynamic shared memory together.
-    cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, kernel);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(kMaxSmemPerCta - fa.sharedSizeBytes));
-    if (e != cudaSuccess) {
-        (void)cudaGetLastError();  // do not leave the error for an unrelated later call
-        return e;
-    }
-    if (cached) done[dev].store(1, std::memory_order_release);
-    return e;
-}
-
-// Launch with programmatic stream serialization: the kernel may be scheduled
-// while the kernel ahead of it in the stream drains, which hides the launch
-// gap between back-to-back calls and between decode and combine.  Both
-// kernels wait (griddepcontrol.wait) before touching memory, so stream order
-// is kept for everything they read and write.
-template <typename... Params>
-cudaError_t launch_pdl(void (*kern)(Params...), unsigned grid, unsigned block, size_t smem,
-                       cudaStream_t st, const Params&... p) {
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(block);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p...);
-    return e != cudaSuccess ? e : cudaGetLastError();
-}
-
 // Forms with a CUDA-core variant for one query head per kv head: bf16 pages.
 template <int D, int B, bool FP8, bool F8MMA>
 constexpr bool has_scalar_form() {
     return !FP8 && !F8MMA;
-}
-
-template <int D, int B, bool FP8, int NH, bool F8MMA, bool SC = false>
-cudaError_t launch_decode(const pa::DecodeParams& p, long long grid, size_t smem,
-                          cudaStream_t st) {
-    static std::atomic<int> done[kMaxDevices];
-    constexpr int W = pa::decode_warps<D, B, FP8>();
-    auto kern = pa::pa_decode_kernel<D, B, FP8, NH, W, F8MMA, SC>;
-    if (smem > kMaxSmemPerCta - kStaticSmemReserve) return cudaErrorInvalidValue;
-    cudaError_t e = ensure_smem(kern, done);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(kern, static_cast<unsigned>(grid), W * 32, smem, st, p);
 }
 
 template <int D, int B, bool FP8, bool F8MMA>
@@ -656,12 +593,14 @@ pa_status check_args(const void* out, const void* query, const void* key_cache,
         if (!aligned(q.p, q.a)) return fail(PA_ERR_INVALID_ARG, "%s is misaligned", q.name);
     }
     if (opts && opts->fp8_compute && kv_dtype != PA_KV_FP8_E4M3)
-        return fail(PA_ERR_INVALID_ARG, "%s", "fp8_compute needs an e4m3 KV cache");
+        return fail(PA_ERR_INVALID_ARG, "%s",
+                    "fp8_compute needs an e4m3 KV cache with per-tensor scales");
     if (opts && opts->alibi_slopes && !aligned(opts->alibi_slopes, 4))
         return fail(PA_ERR_INVALID_ARG, "%s", "alibi_slopes is misaligned");
-    if (kv_dtype == PA_KV_FP8_E4M3) {
+    if (kv_dtype != PA_KV_BF16) {
         if (!k_scale || !v_scale)
-            return fail(PA_ERR_INVALID_ARG, "%s", "k_scale and v_scale are required for FP8");
+            return fail(PA_ERR_INVALID_ARG, "%s",
+                        "k_scale and v_scale are required for an 8-bit cache");
         if (!aligned(k_scale, 4) || !aligned(v_scale, 4))
             return fail(PA_ERR_INVALID_ARG, "%s", "k_scale / v_scale misaligned");
     }
@@ -923,8 +862,12 @@ pa_status pa_decode_ex(void* out, const void* query, const void* key_cache,
         if (e != cudaSuccess) return fail(PA_ERR_CUDA, "combine launch: %s", cudaGetErrorString(e));
         return PA_OK;
     }
-    cudaError_t e = launch_any(p, head_size, block_size, kv_dtype == PA_KV_FP8_E4M3, f8mma, sc,
-                               pl.grid_ctas, pl.smem_bytes, s);
+    cudaError_t e =
+        block_scales(kv_dtype)
+            ? pa::launch_decode_block(p, head_size, block_size, kv_dtype == PA_KV_INT8_BLOCK,
+                                      pl.grid_ctas, pl.smem_bytes, s)
+            : launch_any(p, head_size, block_size, kv_dtype == PA_KV_FP8_E4M3, f8mma, sc,
+                         pl.grid_ctas, pl.smem_bytes, s);
     if (e != cudaSuccess) return fail(PA_ERR_CUDA, "decode launch: %s", cudaGetErrorString(e));
     if (pl.combine) {
         pa::CombineParams c;

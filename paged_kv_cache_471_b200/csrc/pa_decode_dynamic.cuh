@@ -481,14 +481,14 @@ __global__ void __launch_bounds__(W * 32,
         const int pos0 = jg * B - (T - 1);  // ALiBi position of the stage's first slot
         if (!has_alibi) {
             if (full)
-                wa.template page<true, false>(kbase, valid, valid2, pos0);
+                wa.template page<true, false>(kbase, valid, valid2, pos0, PageScales{});
             else
-                wa.template page<false, false>(kbase, valid, valid2, pos0);
+                wa.template page<false, false>(kbase, valid, valid2, pos0, PageScales{});
         } else {
             if (full)
-                wa.template page<true, true>(kbase, valid, valid2, pos0);
+                wa.template page<true, true>(kbase, valid, valid2, pos0, PageScales{});
             else
-                wa.template page<false, true>(kbase, valid, valid2, pos0);
+                wa.template page<false, true>(kbase, valid, valid2, pos0, PageScales{});
         }
         __syncwarp();  // every lane is done with the stage before it is refilled
         --pending;

@@ -22,6 +22,8 @@
 //   * FP8 e4m3 pages are converted in registers (exact e4m3 -> f16) right
 //     before the MMA; k_scale folds into the logit scale and v_scale into the
 //     output, so the conversion needs no multiply (section 4 of the page).
+//   * Codes with a scale per (block, kv head) (KvCodes kE4m3Block, kInt8Block):
+//     see WarpAttn::page for how the scales enter the softmax.
 //   * The warps' (max, sum, acc) are merged in shared memory; the CTA
 //     writes bf16 out directly, or, when the unit is split over several
 //     partitions (or cut at a balanced range's end), an fp32 partial plus its
@@ -59,8 +61,8 @@ struct DecodeParams {
     const uint8_t* vc;        // V cache bytes
     const int32_t* bt;        // [S, max_blocks]
     const int32_t* seq_lens;  // [S]
-    const float* k_scale;     // fp8 only
-    const float* v_scale;     // fp8 only
+    const float* k_scale;     // 8-bit codes: one value, or [num_blocks, Hk] (block scales)
+    const float* v_scale;
     float* ws_o;              // [S, Hq, P, D]   (P > 1)
     float* ws_m;              // [S, Hq, P]      running max, log2 domain
     float* ws_l;              // [S, Hq, P]      running sum
@@ -142,13 +144,64 @@ constexpr int decode_warps() {
     return decode_warps(2LL * D * B * (FP8 ? 1 : 2));
 }
 
+// What an 8-bit page (FP8 forms) holds and where its scales are.
+enum KvCodes : int {
+    kE4m3Tensor = 0,  // e4m3, one k_scale and one v_scale
+    kE4m3Block = 1,   // e4m3, a scale per (block, kv head)
+    kInt8Block = 2    // int8, a scale per (block, kv head)
+};
+
+// A block's scale counts as within [2^-100, 2^100] (a scale of 0 stands for
+// zeros either way), so that log2 of it is finite and the running sums below
+// stay in fp32's range.
+constexpr float kScaleLog2Max = 100.f;
+
+// The scales of the (up to two) pages of a stage: k multiplies the logits,
+// v_log2 is the base-2 logarithm of the V scale.
+struct PageScales {
+    float k[2];
+    float v_log2[2];
+};
+
+// One lane's scales of the pages with ids `id` and `id2` (zeros for an id
+// outside [0, num_blocks), whose page is skipped).
+__device__ __forceinline__ PageScales load_page_scales(const float* k_scale, const float* v_scale,
+                                                       int id, int id2, long long num_blocks,
+                                                       int Hk, int kvh) {
+    PageScales ps;
+    const int ids[2] = {id, id2};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const bool ok = ids[i] >= 0 && static_cast<long long>(ids[i]) < num_blocks;
+        const long long at = ok ? static_cast<long long>(ids[i]) * Hk + kvh : 0;
+        ps.k[i] = ok ? __ldg(k_scale + at) : 0.f;
+        const float v = ok ? log2f(__ldg(v_scale + at)) : 0.f;
+        ps.v_log2[i] = fminf(fmaxf(v, -kScaleLog2Max), kScaleLog2Max);
+    }
+    return ps;
+}
+
+// The scales that lane `src` holds.
+__device__ __forceinline__ PageScales shfl_page_scales(const PageScales& a, int src, bool pair) {
+    PageScales ps = a;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if (i == 1 && !pair) break;
+        ps.k[i] = __shfl_sync(kFull, a.k[i], src);
+        ps.v_log2[i] = __shfl_sync(kFull, a.v_log2[i], src);
+    }
+    return ps;
+}
+
 // One warp's attention state over a run of pages of one unit, and the work
 // on one landed page: the query as MMA operands, the running (max, sum) of
 // its rows and the O^T accumulator, all in registers.  Rows are query heads
 // 8r + gq of the unit (NH blocks of 8 MMA rows); the page body is shared by
 // every schedule of the decode kernel.
-template <int D, int B, bool FP8, int NH, bool F8MMA>
+template <int D, int B, bool FP8, int NH, bool F8MMA, int CODES = kE4m3Tensor>
 struct WarpAttn {
+    static constexpr bool BLOCK = CODES != kE4m3Tensor;  // scales per (block, kv head)
+    static_assert(!BLOCK || (FP8 && !F8MMA), "block scales go with f16 MMAs on 8-bit pages");
     static constexpr int ELEM = FP8 ? 1 : 2;
     static constexpr int K32 = D / 32;  // 32-wide k-steps over the head dim (e4m3 MMA)
     static constexpr int PAGE = D * B * ELEM;  // one K (or V) page of one kv head
@@ -319,6 +372,14 @@ struct WarpAttn {
         }
     }
 
+    // The codes of bytes 0, 1 (lo) or 2, 3 (hi) of a word as two f16 (exact).
+    static __device__ __forceinline__ uint32_t lo_pair(uint32_t w) {
+        return CODES == kInt8Block ? int8_lo_pair(w) : e4m3_lo_pair(w);
+    }
+    static __device__ __forceinline__ uint32_t hi_pair(uint32_t w) {
+        return CODES == kInt8Block ? int8_hi_pair(w) : e4m3_hi_pair(w);
+    }
+
     // Sum each row's l over its quad, so every thread of a quad holds its
     // row's total (before the state leaves the warp).
     __device__ __forceinline__ void reduce_l() {
@@ -407,10 +468,26 @@ struct WarpAttn {
     // One landed page: S = Q K^T, online softmax, O^T += V^T P^T.  FULL pages
     // (every slot a token) skip all masking.
     // `valid` (`valid2`): tokens of the stage's (second) page that count.
+    //
+    // Block scales: a token's logit is x = ks (q . code) and its value vs code,
+    // with ks and vs those of its page.  The weights of the product are
+    // w = vs 2^(x - m) with m the running maximum of x + log2(vs), so that
+    // w <= 1 in f16 whatever the scales; acc sums w code.  The softmax's own
+    // denominator is sum 2^(x - m) = sum w / vs, added up in fp32 from the
+    // unrounded w: a page of zeros (a tiny scale) must still count there,
+    // though its w vanishes in f16.  (m, l, acc) then merge as they always do.
     template <bool FULL, bool ALIBI>
     __device__ __forceinline__ void page(const uint32_t kbase, const int valid, const int valid2,
-                                         const int pos0) {
+                                         const int pos0, const PageScales& ps) {
         const uint32_t vbase = kbase + NPG * PAGE;
+        float mul[NPG], v_inv[NPG];
+        if constexpr (BLOCK) {
+#pragma unroll
+            for (int i = 0; i < NPG; ++i) {
+                mul[i] = qk_mul * ps.k[i];
+                v_inv[i] = fast_exp2(-ps.v_log2[i]);
+            }
+        }
         auto counts = [&](int tk) {  // token tk of the stage is part of the sequence
             if constexpr (PAIR) return tk < B ? tk < valid : tk - B < valid2;
             return tk < valid;
@@ -473,10 +550,10 @@ struct WarpAttn {
                         ldsm_x4(ka, w0, w1, w2, w3);
                         const uint32_t(&qlo)[4] = qa[2 * jp];
                         const uint32_t(&qhi)[4] = qa[2 * jp + 1];
-                        mma_f16_16816(sc[2 * np], qlo, e4m3_lo_pair(w0), e4m3_hi_pair(w0));
-                        mma_f16_16816(sc[2 * np + 1], qlo, e4m3_lo_pair(w1), e4m3_hi_pair(w1));
-                        mma_f16_16816(sc[2 * np], qhi, e4m3_lo_pair(w2), e4m3_hi_pair(w2));
-                        mma_f16_16816(sc[2 * np + 1], qhi, e4m3_lo_pair(w3), e4m3_hi_pair(w3));
+                        mma_f16_16816(sc[2 * np], qlo, lo_pair(w0), hi_pair(w0));
+                        mma_f16_16816(sc[2 * np + 1], qlo, lo_pair(w1), hi_pair(w1));
+                        mma_f16_16816(sc[2 * np], qhi, lo_pair(w2), hi_pair(w2));
+                        mma_f16_16816(sc[2 * np + 1], qhi, lo_pair(w3), hi_pair(w3));
                     }
             }
         }
@@ -493,7 +570,9 @@ struct WarpAttn {
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float x = sc[nt][2 * r + e] * qk_mul;
+                    constexpr int kTilesPerPage = B / 8;
+                    float x = sc[nt][2 * r + e] * (BLOCK ? mul[nt / kTilesPerPage] : qk_mul);
+                    if constexpr (BLOCK) x += ps.v_log2[nt / kTilesPerPage];
                     if constexpr (ALIBI)
                         x = fmaf(slope2[r], static_cast<float>(pos0 + 8 * nt + 2 * cq + e), x);
                     if constexpr (!FULL) {
@@ -527,7 +606,10 @@ struct WarpAttn {
                     ls += bf16_lo(w) + bf16_hi(w);
                 } else {
                     w = pack_f16x2(p0, p1);
-                    ls += f16_lo(w) + f16_hi(w);
+                    if constexpr (BLOCK)
+                        ls = fmaf(p0 + p1, v_inv[nt / (B / 8)], ls);
+                    else
+                        ls += f16_lo(w) + f16_hi(w);
                 }
                 pp[r][nt] = w;
             }
@@ -659,10 +741,8 @@ struct WarpAttn {
                     ldsm_x4(PAIR ? vbase + kk * PAGE + (32 * mp + lane) * B
                                  : vbase + (32 * mp + lane) * B + kk * 16,
                             w0, w1, w2, w3);
-                    uint32_t a0[4] = {e4m3_lo_pair(w0), e4m3_lo_pair(w1), e4m3_hi_pair(w0),
-                                      e4m3_hi_pair(w1)};
-                    uint32_t a1[4] = {e4m3_lo_pair(w2), e4m3_lo_pair(w3), e4m3_hi_pair(w2),
-                                      e4m3_hi_pair(w3)};
+                    uint32_t a0[4] = {lo_pair(w0), lo_pair(w1), hi_pair(w0), hi_pair(w1)};
+                    uint32_t a1[4] = {lo_pair(w2), lo_pair(w3), hi_pair(w2), hi_pair(w3)};
                     if constexpr (!FULL) {
                         a0[0] &= mlo;
                         a0[1] &= mlo;
@@ -702,6 +782,7 @@ struct WarpAttn {
 // The weights stay fp32 (not rounded to bf16 as the MMA operands are).
 template <int D, int B>
 struct WarpAttnScalar {
+    static constexpr bool BLOCK = false;
     static constexpr bool PAIR = pair_pages<D, B, false, false>();
     static constexpr int NPG = PAIR ? 2 : 1;  // logical pages per stage
     static constexpr int BT = B * NPG;        // tokens per stage
@@ -792,7 +873,7 @@ struct WarpAttnScalar {
 
     template <bool FULL, bool ALIBI>
     __device__ __forceinline__ void page(const uint32_t kbase, const int valid, const int valid2,
-                                         const int pos0) {
+                                         const int pos0, const PageScales&) {
         const uint32_t vbase = kbase + NPG * PAGE;
         // ---------------- logits of tokens tl + 8 j (this lane's quarter of the head dims)
         float x[TJ];
@@ -1052,11 +1133,19 @@ __device__ __forceinline__ void prefix_shared_ring(const DecodeParams& p, uint32
     WS wa(lane);
     wa.fetch_query(p.q, row_of);
     float k_scale = 1.f, v_scale = 1.f;
-    if constexpr (FP8) {
+    if constexpr (FP8 && !WS::BLOCK) {
         k_scale = __ldg(p.k_scale);
         v_scale = __ldg(p.v_scale);
     }
     wa.set_alibi(nullptr, p.Hq, row_of);
+    // Block scales: lane l holds those of stage (k & ~31) + l, loaded by every
+    // warp for itself; the ids of the window after it wait in next_id.
+    PageScales scales = {};
+    int next_id = -1, next_id2 = -1;
+    if constexpr (WS::BLOCK) {
+        next_id = load_win(0, 0);
+        if constexpr (PAIR) next_id2 = load_win(0, 1);
+    }
     const size_t head_off = static_cast<size_t>(kvh) * PAGE;
     const size_t block_stride = static_cast<size_t>(p.Hk) * PAGE;
     // Copies of stage i (warp 0 only, stages in increasing order).
@@ -1111,6 +1200,16 @@ __device__ __forceinline__ void prefix_shared_ring(const DecodeParams& p, uint32
     for (; k < span; ++k) {
         const int st = k % nsh;
         const uint32_t ph = static_cast<uint32_t>(k / nsh) & 1u;
+        PageScales ps = {};
+        if constexpr (WS::BLOCK) {
+            if ((k & 31) == 0) {
+                scales = load_page_scales(p.k_scale, p.v_scale, next_id, next_id2, p.num_blocks,
+                                          p.Hk, kvh);
+                next_id = load_win(k + 32, 0);
+                if constexpr (PAIR) next_id2 = load_win(k + 32, 1);
+            }
+            ps = shfl_page_scales(scales, k & 31, PAIR);
+        }
         if (!__all_sync(kFull, mbar_wait_bounded(full0 + 8 * st, ph, p.wait_limit_ns))) {
             timed_out = true;
             break;
@@ -1122,9 +1221,9 @@ __device__ __forceinline__ void prefix_shared_ring(const DecodeParams& p, uint32
         const int valid2 = (fl & 2u) ? B : 0;
         const uint32_t kb = sbase + static_cast<uint32_t>(st * STAGE);
         if (valid == B && (!PAIR || valid2 == B))
-            wa.template page<true, false>(kb, B, B, 0);
+            wa.template page<true, false>(kb, B, B, 0, ps);
         else
-            wa.template page<false, false>(kb, valid, valid2, 0);
+            wa.template page<false, false>(kb, valid, valid2, 0, ps);
         __syncwarp();
         if (lane == 0) mbar_arrive(empty0 + 8 * st);
         if (warp == 0 && issued < span) {
@@ -1155,14 +1254,16 @@ __device__ __forceinline__ void prefix_shared_ring(const DecodeParams& p, uint32
 // The paired 8-row form with f16 MMAs is held to three CTAs per SM (170
 // registers), the residency of the other 8-row forms.
 // SC: one query head per kv head on the CUDA cores (WarpAttnScalar).
-template <int D, int B, bool FP8, int NH, int W, bool F8MMA, bool SC = false>
+template <int D, int B, bool FP8, int NH, int W, bool F8MMA, bool SC = false,
+          int CODES = kE4m3Tensor>
 __global__ void __launch_bounds__(W * 32,
                                   ((pair_pages<D, B, FP8, F8MMA>() && !F8MMA && NH == 1) || SC) ? 3
                                                                                                 : 1)
     pa_decode_kernel(const DecodeParams p) {
     static_assert(!F8MMA || FP8, "e4m3 MMAs need e4m3 pages");
     static_assert(!SC || (!FP8 && NH == 1), "the CUDA-core form takes bf16 pages and one head");
-    using WA = std::conditional_t<SC, WarpAttnScalar<D, B>, WarpAttn<D, B, FP8, NH, F8MMA>>;
+    using WA = std::conditional_t<SC, WarpAttnScalar<D, B>,
+                                  WarpAttn<D, B, FP8, NH, F8MMA, CODES>>;
     constexpr int ELEM = FP8 ? 1 : 2;
     constexpr int PAGE = D * B * ELEM;  // one K (or V) page of one kv head
     // Small pages go in pairs (pair_pages): a stage holds two
@@ -1386,7 +1487,7 @@ __global__ void __launch_bounds__(W * 32,
         WA wa(lane);
         wa.fetch_query(p.q, row_of);
         float k_scale = 1.f, v_scale = 1.f;
-        if constexpr (FP8) {
+        if constexpr (FP8 && !WA::BLOCK) {
             k_scale = __ldg(p.k_scale);
             v_scale = __ldg(p.v_scale);
         }
@@ -1521,8 +1622,20 @@ __global__ void __launch_bounds__(W * 32,
         wa.reset();
 
         bool timed_out = false;
+        // Block scales: lane l holds those of this warp's stage (k & ~31) + l,
+        // loaded at the start of each 32 stages (before the wait for the
+        // stage's pages, which usually takes longer).  win_a then holds those
+        // stages' ids: stages up to k + NS - 1 < k + 32 have been issued.
+        PageScales scales = {};
         int k = 0;
         for (; k < n_my; ++k) {
+            PageScales ps = {};
+            if constexpr (WA::BLOCK) {
+                if ((k & 31) == 0)
+                    scales = load_page_scales(p.k_scale, p.v_scale, win_a, win_a2, p.num_blocks,
+                                              p.Hk, kvh);
+                ps = shfl_page_scales(scales, k & 31, PAIR);
+            }
             const bool landed = mbar_wait_bounded(bar0 + 8 * stage, phase, p.wait_limit_ns);
             if (!__all_sync(kFull, landed)) {
                 timed_out = true;
@@ -1537,14 +1650,14 @@ __global__ void __launch_bounds__(W * 32,
             const int pos0 = jg * B - (T - 1);  // ALiBi position of the stage's first slot
             if (!has_alibi) {
                 if (full)
-                    wa.template page<true, false>(kbase, valid, valid2, pos0);
+                    wa.template page<true, false>(kbase, valid, valid2, pos0, ps);
                 else
-                    wa.template page<false, false>(kbase, valid, valid2, pos0);
+                    wa.template page<false, false>(kbase, valid, valid2, pos0, ps);
             } else {
                 if (full)
-                    wa.template page<true, true>(kbase, valid, valid2, pos0);
+                    wa.template page<true, true>(kbase, valid, valid2, pos0, ps);
                 else
-                    wa.template page<false, true>(kbase, valid, valid2, pos0);
+                    wa.template page<false, true>(kbase, valid, valid2, pos0, ps);
             }
             __syncwarp();
             if (k + NS < n_my) issue(k + NS);

@@ -183,6 +183,17 @@ __device__ __forceinline__ uint32_t e4m3_hi_pair(uint32_t w) {
     return e4m3x2_to_f16x2(static_cast<uint16_t>(w >> 16));
 }
 
+// int8 codes of bytes 0, 1 (lo) or 2, 3 (hi) of a word to two f16 (exact): with
+// its sign bit flipped a code c is the byte c + 128, which under the high byte
+// 0x64 is the f16 number 1024 + 128 + c.
+__device__ __forceinline__ uint32_t int8_pair(uint32_t w, uint32_t select) {
+    const uint32_t h = __byte_perm(w ^ 0x80808080u, 0x64646464u, select);
+    const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&h), __half2half2(__half(1152.f)));
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t int8_lo_pair(uint32_t w) { return int8_pair(w, 0x4140); }
+__device__ __forceinline__ uint32_t int8_hi_pair(uint32_t w) { return int8_pair(w, 0x4342); }
+
 // Two floats to two e4m3 codes (round to nearest even, saturating to +-448);
 // `lo` lands in the low byte.
 __device__ __forceinline__ uint16_t f32x2_to_e4m3x2(float lo, float hi) {
