@@ -332,6 +332,43 @@ pa_status pa_decode_noalloc(void* out, const void* query, const void* key_cache,
                             const float* k_scale, const float* v_scale, void* stream);
 
 /*
+ * Prefill attention: the last n_s tokens of each sequence attend causally over
+ * the sequence's cached keys and values, which include their own (written by
+ * pa_append_kv, say).  Row query_start[s] + i of query, i < n_s =
+ * query_start[s + 1] - query_start[s], is the sequence's token with index
+ * seq_lens[s] - n_s + i and sees the keys 0 .. that index:
+ *     out[row][h] = softmax(scale * q[row][h] . K^T) V   over those keys.
+ * A sequence may have no rows; rows of out that no sequence owns (padding) are
+ * left as they were.  All cache types of pa_decode.
+ *  out, query   bf16 [num_tokens, num_heads, head_size].
+ *  query_start  int32 [num_seqs + 1].
+ *  max_seq_len  upper bound of seq_lens, used only to plan the split.
+ *  opts         NULL, or partition_pages (> 0 splits the keys into partitions
+ *               of that many blocks, rounded up to 128 keys, at most 32 of
+ *               them over max_seq_len) and num_sms; the other fields must be 0
+ *               (PA_ERR_UNSUPPORTED).  By default keys are split only when the
+ *               batch has too few rows for every SM.
+ * Values that a row does not see have no part in it, NaNs and infinities
+ * included.  Everything else, the workspace (pa_prefill_workspace_size bytes;
+ * its status word, and the partials of a split call after the header), the
+ * device-side checks and the errors are as in pa_decode; a query_start outside
+ * [0, num_tokens] or decreasing, or a length below n_s or above the block
+ * table's, skips the sequence (PA_DEV_BAD_QUERY_START,
+ * PA_DEV_SEQ_LEN_OUT_OF_RANGE).
+ */
+size_t pa_prefill_workspace_size(int num_tokens, int num_seqs, int num_heads, int num_kv_heads,
+                                 int head_size, int block_size, int max_seq_len,
+                                 pa_kv_dtype kv_dtype, const pa_options* opts);
+
+pa_status pa_prefill(void* out, const void* query, const void* key_cache, const void* value_cache,
+                     int num_tokens, int num_seqs, int num_heads, int num_kv_heads, int head_size,
+                     float scale, const int32_t* block_tables, int max_blocks_per_seq,
+                     const int32_t* seq_lens, const int32_t* query_start, int block_size,
+                     int max_seq_len, int64_t num_blocks, pa_kv_dtype kv_dtype,
+                     const float* k_scale, const float* v_scale, void* workspace,
+                     size_t workspace_bytes, void* stream, const pa_options* opts);
+
+/*
  * Copy the workspace status word to *flags (synchronises `stream`), and
  * zero it afterwards when clear != 0.
  */

@@ -147,6 +147,12 @@ def _bind(lib):
     lib.pa_append_kv.argtypes = [_P, _P, _P, _P, _I, _I, _I, _I, _P, _I, _P, _P, _I, I64, _I, _P,
                                  _P, _P, _P, ctypes.POINTER(AppendOptions)]
     lib.pa_append_kv.restype = _I
+    lib.pa_prefill.argtypes = [_P, _P, _P, _P, _I, _I, _I, _I, _I, ctypes.c_float, _P, _I, _P, _P,
+                               _I, _I, I64, _I, _P, _P, _P, ctypes.c_size_t, _P,
+                               ctypes.POINTER(Options)]
+    lib.pa_prefill.restype = _I
+    lib.pa_prefill_workspace_size.argtypes = [_I] * 8 + [ctypes.POINTER(Options)]
+    lib.pa_prefill_workspace_size.restype = ctypes.c_size_t
     return lib
 
 
@@ -204,6 +210,22 @@ def plan(num_seqs, num_heads, num_kv_heads, head_size, block_size, max_seq_len, 
                                 _opts(partition_pages, num_sms, stages, shared_prefix_blocks,
                                       None, fp8_compute, False, schedule)))
     return p.as_dict()
+
+
+def prefill_workspace_size(num_tokens, num_seqs, num_heads, num_kv_heads, head_size, block_size,
+                           max_seq_len, kv_dtype="bf16", partition_pages=0, num_sms=0) -> int:
+    n = lib().pa_prefill_workspace_size(num_tokens, num_seqs, num_heads, num_kv_heads, head_size,
+                                        block_size, max_seq_len, kv_dtype_code(kv_dtype),
+                                        _opts(partition_pages, num_sms))
+    if n == 0:
+        raise PagedAttentionError(PA_ERR_INVALID_ARG, lib().pa_last_error_detail().decode())
+    return n
+
+
+@functools.lru_cache(maxsize=4096)
+def _prefill_workspace_size(device, *args):
+    """prefill_workspace_size for the current device (number `device`)."""
+    return prefill_workspace_size(*args)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -388,6 +410,61 @@ def decode(out, query, key_cache, value_cache, num_kv_heads: int, scale: float, 
                                 st.cuda_stream,
                                 _opts(partition_pages, num_sms, stages, shared_prefix_blocks, alibi,
                                       fp8_compute, test_stall_copies, schedule, mha_cuda_cores))
+    _check(rc)
+    return out
+
+
+def prefill(out, query, key_cache, value_cache, num_kv_heads: int, scale: float, block_tables,
+            seq_lens, query_start, block_size: int, max_seq_len: int, kv_dtype="bf16",
+            k_scale=None, v_scale=None, workspace_tensor=None, partition_pages: int = 0,
+            stream=None, num_sms: int = 0):
+    """Causal attention of each sequence's last tokens over its paged cache,
+    into ``out`` (bf16 [num_tokens, num_heads, head_size], like query).
+
+    Rows query_start[s] .. query_start[s + 1] - 1 (int32 [num_seqs + 1]) are
+    the last tokens of sequence s, whose keys and values are in the cache
+    already (append_kv) and counted in seq_lens[s]; a token sees the keys up to
+    its own.  Rows that no sequence owns are left alone.  The cache, its types
+    and scales, the workspace and the stream are those of decode;
+    partition_pages > 0 forces a split of the keys into partitions of that many
+    blocks (by default only batches with few rows are split).
+    """
+    import torch
+    code = kv_dtype_code(kv_dtype)
+    dev = query.device
+    kv_types = _kv_types(code)
+    T, Hq, D = query.shape
+    ptrs = (_ptr(out, "out", (torch.bfloat16,), dev), _ptr(query, "query", (torch.bfloat16,), dev),
+            _ptr(key_cache, "key_cache", kv_types, dev),
+            _ptr(value_cache, "value_cache", kv_types, dev))
+    if out.shape != query.shape:
+        raise ValueError("out must have the query's shape")
+    num_blocks, x = key_cache.shape[0], 16 // key_cache.element_size()
+    if key_cache.shape != (num_blocks, num_kv_heads, D // x, block_size, x) \
+            or value_cache.shape != (num_blocks, num_kv_heads, D, block_size):
+        raise ValueError("cache shapes do not match query / num_kv_heads / block_size")
+    bt = _ptr(block_tables, "block_tables", (torch.int32,), dev)
+    sl = _ptr(seq_lens, "seq_lens", (torch.int32,), dev)
+    qs = _ptr(query_start, "query_start", (torch.int32,), dev)
+    if seq_lens.dim() != 1 or block_tables.dim() != 2 \
+            or block_tables.shape[0] != seq_lens.shape[0] \
+            or query_start.shape != (seq_lens.shape[0] + 1,):
+        raise ValueError("block_tables must be [num_seqs, max_blocks], seq_lens [num_seqs] and "
+                         "query_start [num_seqs + 1]")
+    S = seq_lens.shape[0]
+    ks, vs = _scale_ptrs(code, k_scale, v_scale, num_blocks, num_kv_heads, dev)
+    st = stream if stream is not None else torch.cuda.current_stream(dev)
+    with _on_device(dev):
+        if workspace_tensor is None:  # (a given one is size-checked by the library)
+            need = _prefill_workspace_size(dev.index, T, S, Hq, num_kv_heads, D, block_size,
+                                           max_seq_len, code, partition_pages, num_sms)
+            workspace_tensor = workspace(need, dev, st)
+        rc = lib().pa_prefill(*ptrs, T, S, Hq, int(num_kv_heads), D, float(scale), bt,
+                              block_tables.shape[1], sl, qs, int(block_size), int(max_seq_len),
+                              num_blocks, code, ks, vs,
+                              _ptr(workspace_tensor, "workspace", None, dev),
+                              workspace_tensor.numel() * workspace_tensor.element_size(),
+                              st.cuda_stream, _opts(partition_pages, num_sms))
     _check(rc)
     return out
 

@@ -1,0 +1,959 @@
+// Prefill attention over the paged cache (pa_prefill; see include/pagedattn.h
+// for the contract): the last n_s tokens of each sequence attend causally over
+// the sequence's cached keys and values, their own among them.
+//
+// One CTA per (group of query tokens, kv head, key partition).  Its rows are
+// (query token, head of the kv head's group) pairs, tokens slowest, in two
+// tiles of 128 rows; key tiles of 128 tokens pass by once for all 256 rows:
+//   * warps 8-11 gather the tile's pages into shared memory as tensor-core
+//     operands.  Both page layouts are K-major in 16-byte pieces already (K: 8
+//     head dims of a token, V: 8 tokens of a head dim), so a piece of a bf16
+//     page is one 16-byte asynchronous copy to its place; 8-bit codes are
+//     widened to f16 (exact) on the way;
+//   * warp 12 issues the products: S = Q K^T into TMEM, then O += P V with P
+//     read from TMEM, where it lies over the S it came from;
+//   * warps 0-3 and 4-7 hold a row of one tile per thread: the running maximum
+//     and sum, P = 2^(x - m) back to TMEM.  While one tile is in softmax, the
+//     tensor cores work on the other's products.
+// O is rescaled only when a row's maximum has grown by more than 2^8 since the
+// last time: until then the weights are simply up to 256, which bf16 and f16
+// carry at the same relative precision.
+//
+// Bound: 4 D flops per (row, key) on the tensor cores, against one exponential
+// per (row, key): 16 a clock and SM, so at D = 128 both need the same time.
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cmath>
+#include <cstdio>
+#include <cstring>
+
+#include "pa_launch.cuh"
+#include "pa_tcgen05.cuh"
+#include "pagedattn.h"
+
+namespace pa {
+namespace {
+
+constexpr int kRows = 128;        // rows of a tile (M of the products)
+constexpr int kTiles = 2;         // tiles per CTA
+constexpr int kKeys = 128;        // keys of a tile
+constexpr int kStages = 2;        // K tiles, and V tiles, in shared memory
+constexpr int kInfo = 4;          // key tiles whose page info is kept
+constexpr int kSoftmaxWarps = 8;
+constexpr int kLoadWarps = 4;
+constexpr int kLoadThreads = kLoadWarps * 32;
+constexpr int kMmaWarp = kSoftmaxWarps + kLoadWarps;
+constexpr int kCtaThreads = (kMmaWarp + 1) * 32;
+constexpr uint32_t kTmemColumns = 512;  // S of both tiles, then O of both
+constexpr float kLazyRescale = 8.f;     // log2 of the largest weight
+constexpr int kMaxSplits = 32;          // partials per row (merge_slots)
+constexpr unsigned long long kWaitNs = 2000000000ull;
+
+enum Format : int { kFmtBf16 = 0, kFmtE4m3 = 1, kFmtE4m3Block = 2, kFmtInt8Block = 3 };
+
+struct PrefillParams {
+    __nv_bfloat16* out;          // [T, Hq, D]
+    const uint16_t* q;           // bf16 bits [T, Hq, D]
+    const uint8_t* kc;
+    const uint8_t* vc;
+    const float* k_scale;
+    const float* v_scale;
+    const int32_t* bt;           // [S, max_blocks]
+    const int32_t* seq_lens;     // [S]
+    const int32_t* query_start;  // [S + 1]
+    float* ws_o;                 // [T, Hq, P, D] (P > 1)
+    float* ws_m;                 // [T, Hq, P]
+    float* ws_l;
+    uint32_t* status;
+    long long num_blocks;
+    int T, S, Hq, Hk, G, max_blocks;
+    int tokens_per_tile;   // 128 / G
+    int P, tiles_per_part;
+    int units;             // token groups (an upper bound)
+    float scale_log2;      // |scale| log2(e)
+    int negate;            // scale < 0: the queries are negated
+};
+
+// The sequence of a row or unit: the largest s in [0, S) with first(s) <= x,
+// or -1; `first` does not decrease.  A 32-way search by the whole warp.
+template <class First>
+__device__ __forceinline__ int find_sequence(int S, int lane, First first, int x) {
+    int lo = 0, hi = S;
+    for (;;) {
+        const int step = (hi - lo + 31) / 32;
+        const int i = lo + lane * step;
+        const unsigned before = __ballot_sync(kFull, i < hi && first(i) <= x);
+        if (before == 0) return -1;
+        lo += (__popc(before) - 1) * step;
+        hi = min(hi, lo + step);
+        if (step == 1) return lo;
+    }
+}
+
+template <int D, int FMT>
+struct Layout {  // shared memory, in bytes
+    static constexpr int kTile = kRows * D * 2;  // a Q tile, a K tile or a V tile
+    static constexpr int q = 0;
+    static constexpr int k = q + kTiles * kTile;
+    static constexpr int v = k + kStages * kTile;
+    static constexpr int info = v + kStages * kTile;          // per key tile: 32 floats
+    static constexpr int q_mul = info + kInfo * 32 * 4;       // per row: float
+    static constexpr int bad = q_mul + kTiles * kRows * 4;    // 8 words: see scrub
+    static constexpr int bars = bad + 32;
+    static constexpr int n_bars = 4 * kStages + 2 * kTiles + kInfo + 1;
+    static constexpr int tmem_slot = bars + 8 * n_bars;
+    static constexpr int total = tmem_slot + 16;
+};
+
+// Page info of a key tile: word 0, a bit per page with a legal block id; from
+// word 8, the pages' K scales; from word 16, log2 of their V scales (block
+// formats; 8 pages at most).
+constexpr int kInfoK = 8, kInfoV = 16;
+
+__device__ __forceinline__ bool finite_bf16(uint32_t bits) { return (bits & 0x7f80u) != 0x7f80u; }
+
+template <int D, int B, int FMT>
+__global__ void __launch_bounds__(kCtaThreads, 1) pa_prefill_kernel(const PrefillParams p) {
+    using L = Layout<D, FMT>;
+    constexpr bool BF16 = FMT == kFmtBf16;
+    constexpr bool BLOCK = FMT == kFmtE4m3Block || FMT == kFmtInt8Block;
+    constexpr bool INT8 = FMT == kFmtInt8Block;
+    constexpr int ELEM = BF16 ? 2 : 1;
+    constexpr int PAGE = D * B * ELEM;
+    constexpr int NPG = kKeys / B;  // pages of a key tile
+    extern __shared__ __align__(128) uint8_t smem[];
+    grid_dep_wait();
+    grid_dep_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    // ---------------- this CTA's work; the last units (the longest rows of a
+    // sequence) come first
+    const unsigned per_unit = static_cast<unsigned>(p.Hk) * p.P;
+    const int u = p.units - 1 - static_cast<int>(blockIdx.x / per_unit);
+    const int rest = static_cast<int>(blockIdx.x % per_unit);
+    const int kvh = rest % p.Hk, part = rest / p.Hk;
+    const int tokens_per_cta = kTiles * p.tokens_per_tile;
+    auto first_unit = [&](int s) {
+        return max(0, min(__ldg(p.query_start + s), p.T)) / tokens_per_cta + s;
+    };
+    const int s = find_sequence(p.S, lane, first_unit, u);
+    if (s < 0) return;
+    const int a = __ldg(p.query_start + s), b = __ldg(p.query_start + s + 1);
+    if (a < 0 || b < a || b > p.T) {
+        if (threadIdx.x == 0) atomicOr(p.status, PA_DEV_BAD_QUERY_START);
+        return;
+    }
+    const int n = b - a;
+    const int tok0 = (u - first_unit(s)) * tokens_per_cta;  // first query token of the CTA
+    if (tok0 >= n) return;
+    const int T = __ldg(p.seq_lens + s);
+    if (T < n || T > static_cast<long long>(p.max_blocks) * B) {
+        if (threadIdx.x == 0) atomicOr(p.status, PA_DEV_SEQ_LEN_OUT_OF_RANGE);
+        return;
+    }
+    // Query token i sees the keys [0, T - n + i].  Key tiles of this partition,
+    // for each row tile: [j0, j0 + count(t)).
+    const int seen0 = T - n + tok0 + 1;                                  // by the first row
+    const int seen_end = min(T, seen0 + tokens_per_cta - 1);             // by the last
+    const int j0 = part * p.tiles_per_part;
+    auto count = [&](int t) {
+        if (tok0 + t * p.tokens_per_tile >= n) return 0;
+        const int seen = min(T, seen0 + (t + 1) * p.tokens_per_tile - 1);
+        // (The last partition takes all that is left, also behind max_seq_len.)
+        const int tiles = (seen + kKeys - 1) / kKeys - j0;
+        return max(0, part == p.P - 1 ? tiles : min(tiles, p.tiles_per_part));
+    };
+    const int n0 = count(0), n1 = count(1);
+    const int steps = max(n0, n1);
+
+    const uint32_t sbase = smem_addr(smem);
+    const uint32_t bars = sbase + L::bars;
+    const uint32_t k_full = bars, k_empty = k_full + 8 * kStages, v_full = k_empty + 8 * kStages,
+                   v_empty = v_full + 8 * kStages, s_ready = v_empty + 8 * kStages,
+                   p_ready = s_ready + 8 * kTiles, i_full = p_ready + 8 * kTiles,
+                   drained = i_full + 8 * kInfo;
+    uint32_t* bad = reinterpret_cast<uint32_t*>(smem + L::bad);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(k_full + 8 * i, kLoadThreads);
+            mbar_init(v_full + 8 * i, kLoadThreads);
+            mbar_init(k_empty + 8 * i, 1);
+            mbar_init(v_empty + 8 * i, 1);
+        }
+        for (int t = 0; t < kTiles; ++t) {
+            mbar_init(s_ready + 8 * t, 1);
+            mbar_init(p_ready + 8 * t, kRows);
+        }
+        for (int i = 0; i < kInfo; ++i) mbar_init(i_full + 8 * i, 1);
+        mbar_init(drained, 1);
+        fence_mbar_init();
+        for (int i = 0; i < 8; ++i) bad[i] = 0;
+    }
+    if (warp == kMmaWarp) tmem_alloc(sbase + L::tmem_slot, kTmemColumns);
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::tmem_slot);
+    bool lost = false;  // a wait ran out: leave every loop
+    auto wait_one = [&](uint32_t bar, int phase) {
+        if (!lost && !mbar_wait_bounded(bar, static_cast<uint32_t>(phase) & 1u, kWaitNs))
+            lost = true;
+        return !lost;
+    };
+    auto wait = [&](uint32_t bar, int phase) {  // with the whole warp's verdict
+        lost = !__all_sync(kFull, wait_one(bar, phase));
+        return !lost;
+    };
+
+    if (warp >= kSoftmaxWarps && warp < kMmaWarp) {
+        // ================================================ loaders
+        const int tid = threadIdx.x - kSoftmaxWarps * 32;
+        const int32_t* btrow = p.bt + static_cast<long long>(s) * p.max_blocks;
+        const size_t block_stride = static_cast<size_t>(p.Hk) * PAGE;
+        const size_t head_off = static_cast<size_t>(kvh) * PAGE;
+        // Lane l < NPG: the id of page l of key tile j (-1: none, or not legal).
+        auto page_id = [&](int j) {
+            const int pg = (j0 + j) * NPG + lane;
+            if (lane >= NPG || j >= steps || pg * B >= seen_end) return -1;
+            const int id = __ldg(btrow + pg);
+            if (id >= 0 && id < p.num_blocks) return id;
+            atomicOr(p.status, PA_DEV_BAD_BLOCK_ID);
+            return -1;
+        };
+        int next = page_id(0);
+
+        // The query rows: row r of a tile at 16 r of each 16-byte column, so
+        // that the tile is an operand.  f16 operands (8-bit caches) are scaled
+        // per row by a power of two, which puts the largest |q| in [2^14, 2^15).
+        for (int t = 0; t < kTiles; ++t) {
+            const int qt = tok0 + t * p.tokens_per_tile + tid / p.G;
+            const bool ok = tid < p.tokens_per_tile * p.G && qt < n;
+            const uint4* src = reinterpret_cast<const uint4*>(
+                p.q + ((static_cast<long long>(a) + (ok ? qt : 0)) * p.Hq +
+                       static_cast<long long>(kvh) * p.G + (ok ? tid % p.G : 0)) * D);
+            const uint32_t dst = sbase + L::q + t * L::kTile + tid * 16;
+            const uint32_t flip = p.negate ? 0x80008000u : 0u;
+            float up = 1.f;
+            if constexpr (!BF16) {
+                float amax = 0.f;
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    const uint4 w = ok ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+                    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(x[i])), fabsf(bf16_hi(x[i]))));
+                }
+                int e = 0;  // amax in [2^(14 + e), 2^(15 + e))
+                if (amax > 0.f && amax < INFINITY)
+                    e = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14;
+                e = max(-110, min(113, e));
+                up = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                reinterpret_cast<float*>(smem + L::q_mul)[t * kRows + tid] =
+                    __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+            }
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+                uint4 w = ok ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+                w.x ^= flip;
+                w.y ^= flip;
+                w.z ^= flip;
+                w.w ^= flip;
+                if constexpr (!BF16) {
+                    w.x = pack_f16x2(bf16_lo(w.x) * up, bf16_hi(w.x) * up);
+                    w.y = pack_f16x2(bf16_lo(w.y) * up, bf16_hi(w.y) * up);
+                    w.z = pack_f16x2(bf16_lo(w.z) * up, bf16_hi(w.z) * up);
+                    w.w = pack_f16x2(bf16_lo(w.w) * up, bf16_hi(w.w) * up);
+                }
+                sts128(dst + c * (kRows * 16), w);
+            }
+        }
+
+        auto widen = [&](uint32_t w, uint32_t& lo, uint32_t& hi) {
+            lo = INT8 ? int8_lo_pair(w) : e4m3_lo_pair(w);
+            hi = INT8 ? int8_hi_pair(w) : e4m3_hi_pair(w);
+        };
+        auto put16 = [&](uint32_t lo_at, uint32_t hi_at, const uint4& w) {  // 16 codes
+            uint4 x, y;
+            widen(w.x, x.x, x.y);
+            widen(w.y, x.z, x.w);
+            widen(w.z, y.x, y.y);
+            widen(w.w, y.z, y.w);
+            sts128(lo_at, x);
+            sts128(hi_at, y);
+        };
+
+        for (int j = 0; j < steps && !lost; ++j) {
+            const int st = j % kStages, round = j / kStages;
+            const int ids = next;
+            next = page_id(j + 1);
+            const int key0 = (j0 + j) * kKeys;
+            if (warp == kSoftmaxWarps) {
+                // Page info for the softmax warps (kInfo tiles deep: the slot's
+                // last user is done once K of tile j - 2 has been released).
+                float* info = reinterpret_cast<float*>(smem + L::info) + (j % kInfo) * 32;
+                if (!wait(k_empty + 8 * st, round + 1)) break;
+                const unsigned legal = __ballot_sync(kFull, lane < NPG && ids >= 0);
+                if (lane == 0) reinterpret_cast<uint32_t*>(info)[0] = legal;
+                if constexpr (BLOCK) {
+                    if (lane < NPG) {
+                        const PageScales ps = load_page_scales(p.k_scale, p.v_scale, ids, -1,
+                                                               p.num_blocks, p.Hk, kvh);
+                        info[kInfoK + lane] = ps.k[0];
+                        info[kInfoV + lane] = ps.v_log2[0];
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(i_full + 8 * (j % kInfo));
+            }
+            const uint32_t kdst = sbase + L::k + st * L::kTile;
+            const uint32_t vdst = sbase + L::v + st * L::kTile;
+            // Tiles with keys that some row does not see: non-finite values of
+            // those are kept out of the product (0 times NaN is NaN) and noted
+            // for the rows that do see them.
+            const bool edge = key0 + kKeys > seen0;
+            auto scrub = [&](uint4& w, int key, int count_keys) {  // keys of one head dim, bf16
+                uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if (e >= count_keys) break;
+                    const uint32_t v = (x[e / 2] >> (16 * (e % 2))) & 0xffffu;
+                    const bool hidden = key + e >= seen_end;
+                    if (key + e < seen0 || (finite_bf16(v) && !hidden)) continue;
+                    x[e / 2] &= e % 2 ? 0x0000ffffu : 0xffff0000u;
+                    if (!hidden) {
+                        const int i = key + e - seen0;
+                        atomicOr(bad + (i >> 5), 1u << (i & 31));
+                    }
+                }
+                w = make_uint4(x[0], x[1], x[2], x[3]);
+            };
+            auto scrub_codes = [&](uint32_t w, int key) {  // 4 keys of one head dim
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t v = (w >> (8 * e)) & 0x7fu;
+                    const bool hidden = key + e >= seen_end;
+                    if (key + e < seen0 || ((INT8 || v != 0x7fu) && !hidden)) continue;
+                    w &= ~(0xffu << (8 * e));
+                    if (!hidden) {
+                        const int i = key + e - seen0;
+                        atomicOr(bad + (i >> 5), 1u << (i & 31));
+                    }
+                }
+                return w;
+            };
+            if constexpr (BF16) {
+                // ---- K: pieces (column group c, token) of a page are contiguous
+                constexpr int KP = D / 8 * B;  // pieces of a page
+                if (!wait(k_empty + 8 * st, round + 1)) break;
+#pragma unroll 4
+                for (int i = tid; i < NPG * KP; i += kLoadThreads) {
+                    const int pg = i / KP, c = i % KP / B, tk = i % B;
+                    const int id = __shfl_sync(kFull, ids, pg);
+                    cp_async16(kdst + c * (kKeys * 16) + (pg * B + tk) * 16,
+                               p.kc + (id < 0 ? 0 : id) * block_stride + head_off + i % KP * 16,
+                               id < 0 ? 0u : 16u);
+                }
+                cp_async_commit();
+                if (j > 0) {  // V of the tile before has landed
+                    cp_async_wait<1>();
+                    fence_smem_to_async();
+                    mbar_arrive(v_full + 8 * ((j - 1) % kStages));
+                }
+                // ---- V: pieces (head dim, 8 tokens); a warp covers whole rows
+                constexpr int VR = B / 8, RW = 32 / VR;  // pieces of a row, rows per warp
+                constexpr int VP = D * VR;
+                if (!wait(v_empty + 8 * st, round + 1)) break;
+#pragma unroll 4
+                for (int i = tid; i < NPG * VP; i += kLoadThreads) {
+                    const int pg = i / VP, in_page = i % VP;
+                    const int d = in_page / 32 * RW + lane % RW, h = lane / RW;
+                    const int id = __shfl_sync(kFull, ids, pg);
+                    const uint8_t* src = p.vc + (id < 0 ? 0 : id) * block_stride + head_off +
+                                         (d * B + h * 8) * 2;
+                    const uint32_t dst = vdst + (pg * VR + h) * (D * 16) + d * 16;
+                    if (edge) {
+                        uint4 w = id < 0 ? make_uint4(0, 0, 0, 0)
+                                         : __ldg(reinterpret_cast<const uint4*>(src));
+                        scrub(w, key0 + pg * B + h * 8, 8);
+                        sts128(dst, w);
+                    } else {
+                        cp_async16(dst, src, id < 0 ? 0u : 16u);
+                    }
+                }
+                cp_async_commit();
+                cp_async_wait<1>();  // K has landed
+                fence_smem_to_async();
+                mbar_arrive(k_full + 8 * st);
+            } else {
+                // ---- K: pieces (16 head dims, token); V: pieces (head dim, 16 tokens)
+                constexpr int KP = D / 16 * B, VR = B / 16, VP = D * VR;
+                constexpr int IT = NPG * KP / kLoadThreads;  // pieces per thread
+                static_assert(NPG * KP == NPG * VP && NPG * KP % kLoadThreads == 0, "");
+                uint4 w[IT];
+#pragma unroll
+                for (int k = 0; k < IT; ++k) {
+                    const int i = tid + k * kLoadThreads, pg = i / KP;
+                    const int id = __shfl_sync(kFull, ids, pg);
+                    w[k] = id < 0 ? make_uint4(0, 0, 0, 0)
+                                  : __ldg(reinterpret_cast<const uint4*>(
+                                        p.kc + id * block_stride + head_off + i % KP * 16));
+                }
+                if (!wait(k_empty + 8 * st, round + 1)) break;
+#pragma unroll
+                for (int k = 0; k < IT; ++k) {
+                    const int i = tid + k * kLoadThreads;
+                    const int pg = i / KP, c = i % KP / B, tk = i % B;
+                    const uint32_t at = kdst + 2 * c * (kKeys * 16) + (pg * B + tk) * 16;
+                    put16(at, at + kKeys * 16, w[k]);
+                }
+                fence_smem_to_async();
+                mbar_arrive(k_full + 8 * st);
+#pragma unroll
+                for (int k = 0; k < IT; ++k) {
+                    const int i = tid + k * kLoadThreads, pg = i / VP;
+                    const int d = VR == 1 ? i % VP : i % VP / 32 * 16 + lane % 16;
+                    const int h = VR == 1 ? 0 : lane / 16;
+                    const int id = __shfl_sync(kFull, ids, pg);
+                    w[k] = id < 0 ? make_uint4(0, 0, 0, 0)
+                                  : __ldg(reinterpret_cast<const uint4*>(
+                                        p.vc + id * block_stride + head_off + d * B + h * 16));
+                    if (edge) {
+                        const int key = key0 + pg * B + h * 16;
+                        w[k].x = scrub_codes(w[k].x, key);
+                        w[k].y = scrub_codes(w[k].y, key + 4);
+                        w[k].z = scrub_codes(w[k].z, key + 8);
+                        w[k].w = scrub_codes(w[k].w, key + 12);
+                    }
+                }
+                if (!wait(v_empty + 8 * st, round + 1)) break;
+#pragma unroll
+                for (int k = 0; k < IT; ++k) {
+                    const int i = tid + k * kLoadThreads, pg = i / VP;
+                    const int d = VR == 1 ? i % VP : i % VP / 32 * 16 + lane % 16;
+                    const int h = VR == 1 ? 0 : lane / 16;
+                    const uint32_t at = vdst + 2 * (pg * VR + h) * (D * 16) + d * 16;
+                    put16(at, at + D * 16, w[k]);
+                }
+                fence_smem_to_async();
+                mbar_arrive(v_full + 8 * st);
+            }
+        }
+        if constexpr (BF16) {
+            cp_async_wait<0>();
+            if (!lost && steps > 0) {
+                fence_smem_to_async();
+                mbar_arrive(v_full + 8 * ((steps - 1) % kStages));
+            }
+        }
+    } else if (warp == kMmaWarp) {
+        // ================================================ products
+        if (lane == 0) {
+            constexpr uint32_t kQk = mma_shape(BF16, kRows, kKeys);
+            constexpr uint32_t kPv = mma_shape(BF16, kRows, D);
+            auto scores = [&](int t, int st) {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    mma_ss(tmem + t * kKeys,
+                           smem_operand(sbase + L::q + t * L::kTile + k * (2 * kRows * 16),
+                                        kRows * 16),
+                           smem_operand(sbase + L::k + st * L::kTile + k * (2 * kKeys * 16),
+                                        kKeys * 16),
+                           kQk, k > 0);
+            };
+            auto values = [&](int t, int st, bool add) {
+#pragma unroll
+                for (int k = 0; k < kKeys / 16; ++k)
+                    mma_ts(tmem + kTiles * kKeys + t * 128, tmem + t * kKeys + 8 * k,
+                           smem_operand(sbase + L::v + st * L::kTile + k * (2 * D * 16), D * 16),
+                           kPv, add || k > 0);
+            };
+            if (steps > 0 && wait_one(k_full, 0)) {
+                tmem_fence_after();
+                if (n0 > 0) {
+                    scores(0, 0);
+                    mma_commit(s_ready);
+                }
+                if (n1 > 0) {
+                    scores(1, 0);
+                    mma_commit(s_ready + 8);
+                }
+                mma_commit(k_empty);
+            }
+            for (int j = 0; j < steps && !lost; ++j) {
+                const int st = j % kStages, nx = (j + 1) % kStages;
+                if (!wait_one(v_full + 8 * st, j / kStages)) break;
+                for (int t = 0; t < kTiles; ++t) {
+                    const int nt = t ? n1 : n0;
+                    if (j >= nt) continue;
+                    if (!wait_one(p_ready + 8 * t, j)) break;
+                    tmem_fence_after();
+                    values(t, st, j > 0);
+                    if (j + 1 < nt) {
+                        if (!wait_one(k_full + 8 * nx, (j + 1) / kStages)) break;
+                        tmem_fence_after();
+                        scores(t, nx);
+                    }
+                    // S of the next tile, or O, is there (and P consumed).
+                    mma_commit(s_ready + 8 * t);
+                }
+                if (lost) break;
+                mma_commit(v_empty + 8 * st);
+                if (j + 1 < steps) mma_commit(k_empty + 8 * nx);
+            }
+            if (lost) {
+                // The products in flight still write TMEM: wait for them (bounded).
+                mma_commit(drained);
+                (void)mbar_wait_bounded(drained, 0u, kWaitNs);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ================================================ softmax, one row per thread
+        const int t = warp / 4;
+        const int r = threadIdx.x - t * kRows;
+        const int nt = t ? n1 : n0;
+        const uint32_t lanes = static_cast<uint32_t>(warp % 4 * 32) << 16;
+        const uint32_t s_at = tmem + lanes + t * kKeys;
+        const uint32_t o_at = tmem + lanes + kTiles * kKeys + t * 128;
+        const int qt = tok0 + t * p.tokens_per_tile + r / p.G;
+        const bool row_ok = r < p.tokens_per_tile * p.G && qt < n;
+        // Keys of this row; a row of no query token counts as seeing all, so that
+        // it does not make its warp mask (its results go nowhere).
+        const int seen = row_ok ? T - n + qt + 1 : 0x7fffffff;
+        float mul = p.scale_log2, out_mul = 1.f;
+        float m = -INFINITY, l = 0.f;
+        for (int j = 0; j < nt && !lost; ++j) {
+            if (!wait(s_ready + 8 * t, j)) break;
+            if (!wait(i_full + 8 * (j % kInfo), j / kInfo)) break;
+            tmem_fence_after();
+            if constexpr (!BF16) {
+                if (j == 0) {
+                    mul *= reinterpret_cast<const float*>(smem + L::q_mul)[t * kRows + r];
+                    if constexpr (!BLOCK) {
+                        mul *= fabsf(__ldg(p.k_scale));
+                        out_mul = __ldg(p.v_scale);
+                    }
+                }
+            }
+            const float* info = reinterpret_cast<const float*>(smem + L::info) + (j % kInfo) * 32;
+            const uint32_t legal = reinterpret_cast<const uint32_t*>(info)[0];
+            const int left = seen - (j0 + j) * kKeys;  // keys of this tile that the row sees
+            const bool masked =
+                __any_sync(kFull, left < kKeys) || legal != (1u << NPG) - 1u;
+            // A column's score, -inf where the row does not see its key.
+            auto visible = [&](int c) {
+                return c < left && ((legal >> (c / B)) & 1u);
+            };
+            uint32_t x[32];
+            // ---- the tile's maximum (of x + log2 vs with block scales)
+            float mx = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < kKeys; c += 32) {
+                tmem_ld32(s_at + c, x);
+                tmem_wait_ld();
+                if (masked) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (!visible(c + i)) x[i] = 0xff800000u;
+                }
+#pragma unroll
+                for (int g = 0; g < 32; g += 16) {
+                    float y = __uint_as_float(x[g]);
+#pragma unroll
+                    for (int i = 1; i < 16; ++i) y = fmaxf(y, __uint_as_float(x[g + i]));
+                    const int pg = (c + g) / B;
+                    if constexpr (BLOCK) {
+                        // (-inf stays: a page's scale of 0 must not make it NaN)
+                        const float z = fmaf(y, mul * info[kInfoK + pg], info[kInfoV + pg]);
+                        y = y == -INFINITY ? y : z;
+                    }
+                    mx = fmaxf(mx, y);
+                }
+            }
+            if constexpr (!BLOCK) mx = mx == -INFINITY ? mx : mx * mul;
+            // ---- O in the units of a new maximum, only when it grew by a lot
+            const bool grow = mx > m + kLazyRescale || (m == -INFINITY && mx > -INFINITY);
+            if (__any_sync(kFull, grow)) {
+                const float to = grow ? mx : m;
+                const float alpha = to == -INFINITY ? 1.f : fast_exp2(m - to);
+                m = to;
+                l *= alpha;
+                if (j > 0) {
+#pragma unroll
+                    for (int c = 0; c < D; c += 32) {
+                        tmem_ld32(o_at + c, x);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            x[i] = __float_as_uint(__uint_as_float(x[i]) * alpha);
+                        tmem_st32(o_at + c, x);
+                    }
+                }
+            }
+            const float m_use = m == -INFINITY ? 0.f : m;
+            // ---- weights back to TMEM over the scores; their sum
+#pragma unroll
+            for (int c = 0; c < kKeys; c += 32) {
+                tmem_ld32(s_at + c, x);
+                tmem_wait_ld();
+                if (masked) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (!visible(c + i)) x[i] = 0xff800000u;
+                }
+                uint32_t w[16];
+#pragma unroll
+                for (int g = 0; g < 32; g += 16) {
+                    const int pg = (c + g) / B;
+                    float f = mul, add = -m_use, back = 1.f;
+                    if constexpr (BLOCK) {
+                        f = mul * info[kInfoK + pg];
+                        add = info[kInfoV + pg] - m_use;
+                        back = fast_exp2(-info[kInfoV + pg]);
+                    }
+                    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) {
+                        float y0 = fmaf(__uint_as_float(x[g + i]), f, add);
+                        float y1 = fmaf(__uint_as_float(x[g + i + 1]), f, add);
+                        if (masked) {  // a factor of 0 makes NaN of -inf
+                            if (x[g + i] == 0xff800000u) y0 = -INFINITY;
+                            if (x[g + i + 1] == 0xff800000u) y1 = -INFINITY;
+                        }
+                        const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
+                        s0 += p0;
+                        s1 += p1;
+                        w[(g + i) / 2] = BF16 ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
+                    }
+                    l = BLOCK ? fmaf(s0 + s1, back, l) : l + (s0 + s1);
+                }
+                tmem_st16(s_at + c / 2, w);
+            }
+            tmem_wait_st();
+            tmem_fence_before();
+            mbar_arrive(p_ready + 8 * t);
+        }
+        // ---- the rows' results
+        if (nt > 0) (void)wait(s_ready + 8 * t, nt);
+        tmem_fence_after();
+        const int head = kvh * p.G + r % p.G;
+        const long long row = (static_cast<long long>(a) + qt) * p.Hq + head;
+        const long long prow = row * p.P + part;
+        const bool empty = nt == 0 || lost;
+        if (p.P > 1 && row_ok) {
+            // (A sum of NaN goes to the merge as an overriding row of NaNs.)
+            p.ws_m[prow] = l != l ? 1e30f : m;
+            p.ws_l[prow] = empty ? 0.f : l != l ? 1.f : l;
+        }
+        const float inv = l > 0.f || l != l ? out_mul / l : 0.f;
+        if (nt > 0) {
+            uint32_t any_bad = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) any_bad |= bad[i];
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+                uint32_t x[32];
+                tmem_ld32(o_at + c, x);
+                tmem_wait_ld();
+                float o[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(x[i]);
+                if (any_bad && row_ok) {
+                    // Non-finite values of keys that not every row of the CTA
+                    // sees were left out: they make the rows that do see them
+                    // what they are.
+                    for (int key = seen0; key < seen; ++key) {
+                        if (!((bad[(key - seen0) >> 5] >> ((key - seen0) & 31)) & 1u)) continue;
+                        const int jk = key / kKeys - j0;
+                        if (jk < 0 || jk >= nt) continue;  // another partition's
+                        const int id = __ldg(p.bt + static_cast<long long>(s) * p.max_blocks +
+                                             key / B);
+                        if (id < 0 || id >= p.num_blocks) continue;
+                        const uint8_t* v = p.vc + static_cast<size_t>(id) * p.Hk * PAGE +
+                                           static_cast<size_t>(kvh) * PAGE;
+                        for (int i = 0; i < 32; ++i) {
+                            const int at = (c + i) * B + key % B;
+                            float y = 0.f;
+                            if constexpr (BF16) {
+                                y = __uint_as_float(static_cast<uint32_t>(
+                                        __ldg(reinterpret_cast<const uint16_t*>(v) + at)) << 16);
+                            } else if constexpr (!INT8) {
+                                y = (__ldg(v + at) & 0x7f) == 0x7f ? NAN : 0.f;
+                            }
+                            if (!(fabsf(y) < INFINITY)) {
+#pragma unroll
+                                for (int k = 0; k < 32; ++k)
+                                    if (k == i) o[k] += y;
+                            }
+                        }
+                    }
+                }
+                if (!row_ok || lost) continue;
+                if (p.P > 1) {
+                    float4* dst = reinterpret_cast<float4*>(p.ws_o + prow * D + c);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        dst[i] = make_float4(o[4 * i] * inv, o[4 * i + 1] * inv,
+                                             o[4 * i + 2] * inv, o[4 * i + 3] * inv);
+                } else {
+                    uint4* dst = reinterpret_cast<uint4*>(p.out + row * D + c);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        dst[i] = make_uint4(pack_bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv),
+                                            pack_bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                            pack_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                                            pack_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+                }
+            }
+        }
+    }
+    if (lost && lane == 0) atomicOr(p.status, PA_DEV_WAIT_TIMEOUT);
+    tmem_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tmem_fence_after();
+        tmem_free(tmem, kTmemColumns);
+    }
+}
+
+// Merges the P partials of each (token, head) row, a warp per row.  Rows that
+// no sequence owns, or whose sequence was skipped, are left alone.
+template <int D>
+__global__ void __launch_bounds__(kThreads)
+    pa_prefill_merge_kernel(const PrefillParams p, int block_size) {
+    grid_dep_wait();
+    grid_dep_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long row = static_cast<long long>(blockIdx.x) * kWarps + warp;
+    if (row >= static_cast<long long>(p.T) * p.Hq) return;
+    merge_slots<D>(p.ws_o, p.ws_m, p.ws_l, p.out, row * p.P, p.P, lane, [&]() -> SlotRow {
+        const int token = static_cast<int>(row / p.Hq);
+        const int s = find_sequence(
+            p.S, lane, [&](int i) { return max(0, min(__ldg(p.query_start + i), p.T)); }, token);
+        if (s < 0) return {-1, row};
+        const int a = __ldg(p.query_start + s), b = __ldg(p.query_start + s + 1);
+        const int len = __ldg(p.seq_lens + s);
+        const bool mine = a >= 0 && b <= p.T && token >= a && token < b && len >= b - a &&
+                          len <= static_cast<long long>(p.max_blocks) * block_size;
+        return {mine ? p.P : -1, row};
+    });
+}
+
+template <int D, int B, int FMT>
+cudaError_t launch_prefill(const PrefillParams& p, unsigned grid, cudaStream_t st) {
+    static std::atomic<int> done[kMaxDevices];
+    auto kern = pa_prefill_kernel<D, B, FMT>;
+    cudaError_t e = ensure_smem(kern, done);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, grid, kCtaThreads, Layout<D, FMT>::total, st, p);
+}
+
+template <int D, int B>
+cudaError_t launch_format(const PrefillParams& p, pa_kv_dtype t, unsigned grid, cudaStream_t st) {
+    switch (t) {
+        case PA_KV_BF16: return launch_prefill<D, B, kFmtBf16>(p, grid, st);
+        case PA_KV_FP8_E4M3: return launch_prefill<D, B, kFmtE4m3>(p, grid, st);
+        case PA_KV_FP8_E4M3_BLOCK: return launch_prefill<D, B, kFmtE4m3Block>(p, grid, st);
+        default: return launch_prefill<D, B, kFmtInt8Block>(p, grid, st);
+    }
+}
+
+struct PrefillPlan {
+    long long units;
+    int P, tiles_per_part;
+    size_t workspace_bytes;
+};
+
+pa_status check_sizes(int num_tokens, int num_seqs, int num_heads,
+                      int num_kv_heads, int head_size, int block_size, int max_seq_len,
+                      pa_kv_dtype kv_dtype, const pa_options* opts) {
+    if (num_tokens < 0 || num_seqs < 0)
+        return fail(PA_ERR_INVALID_ARG, "%s", "num_tokens or num_seqs < 0");
+    if (num_heads <= 0 || num_kv_heads <= 0)
+        return fail(PA_ERR_INVALID_ARG, "%s", "num_heads and num_kv_heads must be > 0");
+    if (num_heads % num_kv_heads)
+        return fail(PA_ERR_INVALID_ARG, "%s", "num_heads must be a multiple of num_kv_heads");
+    if (num_heads / num_kv_heads > 16)
+        return fail(PA_ERR_UNSUPPORTED, "%s", "num_heads / num_kv_heads > 16");
+    if (head_size != 64 && head_size != 128)
+        return fail(PA_ERR_UNSUPPORTED, "%s", "head_size must be 64 or 128");
+    if (block_size != 16 && block_size != 32)
+        return fail(PA_ERR_UNSUPPORTED, "%s", "block_size must be 16 or 32");
+    if (kv_dtype != PA_KV_BF16 && kv_dtype != PA_KV_FP8_E4M3 && !block_scales(kv_dtype))
+        return fail(PA_ERR_UNSUPPORTED, "%s", "kv_dtype");
+    if (max_seq_len < 0) return fail(PA_ERR_INVALID_ARG, "%s", "max_seq_len < 0");
+    if (opts) {
+        if (opts->num_sms < 0 || opts->partition_pages < 0)
+            return fail(PA_ERR_INVALID_ARG, "%s", "opts->num_sms or opts->partition_pages < 0");
+        if (opts->stages || opts->shared_prefix_blocks || opts->alibi_slopes ||
+            opts->fp8_compute || opts->test_stall_copies || opts->schedule || opts->mha_cuda_cores)
+            return fail(PA_ERR_UNSUPPORTED, "%s",
+                        "prefill takes partition_pages and num_sms only");
+    }
+    return PA_OK;
+}
+
+// Sizes that check_sizes has passed.
+pa_status plan_prefill(PrefillPlan* pl, int num_tokens, int num_seqs, int num_heads,
+                       int num_kv_heads, int head_size, int block_size, int max_seq_len,
+                       const pa_options* opts) {
+    int sms = opts ? opts->num_sms : 0;
+    if (sms == 0 && device_sms(&sms) != 0)
+        return fail(PA_ERR_CUDA, "%s", "cannot query the SM count of the current device");
+    const int tokens_per_cta = kTiles * (kRows / (num_heads / num_kv_heads));
+    pl->units = num_tokens / tokens_per_cta + static_cast<long long>(num_seqs);
+    const long long ctas = pl->units * num_kv_heads;
+    const long long tiles = (static_cast<long long>(max_seq_len) + kKeys - 1) / kKeys;
+    long long per;
+    if (opts && opts->partition_pages > 0) {
+        per = (static_cast<long long>(opts->partition_pages) * block_size + kKeys - 1) / kKeys;
+    } else {
+        // A batch whose CTAs leave SMs idle splits the keys, two tiles at least
+        // to a partition, so that about every SM has a CTA.
+        long long P = ctas > 0 ? sms / ctas : 1;
+        if (P > tiles / 2) P = tiles / 2;
+        if (P > kMaxSplits) P = kMaxSplits;
+        if (P < 1) P = 1;
+        per = (tiles + P - 1) / P;
+    }
+    if (per < 1) per = 1;
+    const long long P = tiles > 0 ? (tiles + per - 1) / per : 1;
+    if (P > kMaxSplits)
+        return fail(PA_ERR_INVALID_ARG, "%s",
+                    "opts->partition_pages makes more than 32 partitions of max_seq_len");
+    if (ctas * P > 0x7fffffffll ||
+        static_cast<long long>(num_tokens) * num_heads > 0x7fffffffll)
+        return fail(PA_ERR_INVALID_ARG, "%s", "too many tokens, sequences and heads for one call");
+    pl->P = static_cast<int>(P);
+    pl->tiles_per_part = static_cast<int>(per);
+    pl->workspace_bytes = PA_WORKSPACE_HEADER_BYTES;
+    if (P > 1) {
+        pl->workspace_bytes += static_cast<size_t>(num_tokens) * num_heads * P *
+                               (static_cast<size_t>(head_size) + 2) * sizeof(float);
+        pl->workspace_bytes = (pl->workspace_bytes + 255) & ~static_cast<size_t>(255);
+    }
+    return PA_OK;
+}
+
+}  // namespace
+}  // namespace pa
+
+extern "C" size_t pa_prefill_workspace_size(int num_tokens, int num_seqs, int num_heads,
+                                            int num_kv_heads, int head_size, int block_size,
+                                            int max_seq_len, pa_kv_dtype kv_dtype,
+                                            const pa_options* opts) {
+    pa::clear_detail();
+    pa::PrefillPlan pl;
+    if (pa::check_sizes(num_tokens, num_seqs, num_heads, num_kv_heads, head_size, block_size,
+                        max_seq_len, kv_dtype, opts) != PA_OK ||
+        pa::plan_prefill(&pl, num_tokens, num_seqs, num_heads, num_kv_heads, head_size, block_size,
+                         max_seq_len, opts) != PA_OK)
+        return 0;
+    return pl.workspace_bytes;
+}
+
+extern "C" pa_status pa_prefill(void* out, const void* query, const void* key_cache,
+                                const void* value_cache, int num_tokens, int num_seqs,
+                                int num_heads, int num_kv_heads, int head_size, float scale,
+                                const int32_t* block_tables, int max_blocks_per_seq,
+                                const int32_t* seq_lens, const int32_t* query_start,
+                                int block_size, int max_seq_len, int64_t num_blocks,
+                                pa_kv_dtype kv_dtype, const float* k_scale, const float* v_scale,
+                                void* workspace, size_t workspace_bytes, void* stream,
+                                const pa_options* opts) {
+    using pa::aligned;
+    using pa::fail;
+    pa::clear_detail();
+    pa_status status = pa::check_sizes(num_tokens, num_seqs, num_heads, num_kv_heads, head_size,
+                                       block_size, max_seq_len, kv_dtype, opts);
+    if (status != PA_OK) return status;
+    if (!std::isfinite(scale)) return fail(PA_ERR_INVALID_ARG, "%s", "scale is not finite");
+    if (max_blocks_per_seq < 1) return fail(PA_ERR_INVALID_ARG, "%s", "max_blocks_per_seq < 1");
+    if (static_cast<long long>(max_seq_len) >
+        static_cast<long long>(max_blocks_per_seq) * block_size)
+        return fail(PA_ERR_INVALID_ARG, "%s", "max_seq_len > max_blocks_per_seq * block_size");
+    if (num_blocks < 1) return fail(PA_ERR_INVALID_ARG, "%s", "num_blocks < 1");
+    if (num_tokens == 0 || num_seqs == 0) return PA_OK;
+    const struct {
+        const void* p;
+        size_t a;
+        const char* name;
+    } ptrs[] = {{out, 16, "out"},
+                {query, 16, "query"},
+                {key_cache, 16, "key_cache"},
+                {value_cache, 16, "value_cache"},
+                {block_tables, 4, "block_tables"},
+                {seq_lens, 4, "seq_lens"},
+                {query_start, 4, "query_start"},
+                {workspace, 16, "workspace"}};
+    for (const auto& q : ptrs) {
+        if (!q.p) return fail(PA_ERR_INVALID_ARG, "%s is NULL", q.name);
+        if (!aligned(q.p, q.a)) return fail(PA_ERR_INVALID_ARG, "%s is misaligned", q.name);
+    }
+    if (kv_dtype != PA_KV_BF16) {
+        if (!k_scale || !v_scale)
+            return fail(PA_ERR_INVALID_ARG, "%s",
+                        "k_scale and v_scale are required for an 8-bit cache");
+        if (!aligned(k_scale, 4) || !aligned(v_scale, 4))
+            return fail(PA_ERR_INVALID_ARG, "%s", "k_scale / v_scale misaligned");
+    }
+    pa::PrefillPlan pl;
+    status = pa::plan_prefill(&pl, num_tokens, num_seqs, num_heads, num_kv_heads, head_size,
+                              block_size, max_seq_len, opts);
+    if (status != PA_OK) return status;
+    if (workspace_bytes < pl.workspace_bytes)
+        return fail(PA_ERR_WORKSPACE_TOO_SMALL, "%s",
+                    "workspace_bytes < pa_prefill_workspace_size");
+    pa::PrefillParams p;
+    std::memset(&p, 0, sizeof p);
+    p.out = static_cast<__nv_bfloat16*>(out);
+    p.q = static_cast<const uint16_t*>(query);
+    p.kc = static_cast<const uint8_t*>(key_cache);
+    p.vc = static_cast<const uint8_t*>(value_cache);
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.bt = block_tables;
+    p.seq_lens = seq_lens;
+    p.query_start = query_start;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const size_t rows = static_cast<size_t>(num_tokens) * num_heads * pl.P;
+    p.ws_o = reinterpret_cast<float*>(ws + PA_WORKSPACE_HEADER_BYTES);
+    p.ws_m = p.ws_o + rows * head_size;
+    p.ws_l = p.ws_m + rows;
+    p.status = reinterpret_cast<uint32_t*>(ws);
+    p.num_blocks = num_blocks;
+    p.T = num_tokens;
+    p.S = num_seqs;
+    p.Hq = num_heads;
+    p.Hk = num_kv_heads;
+    p.G = num_heads / num_kv_heads;
+    p.max_blocks = max_blocks_per_seq;
+    p.tokens_per_tile = pa::kRows / p.G;
+    p.P = pl.P;
+    p.tiles_per_part = pl.tiles_per_part;
+    p.units = static_cast<int>(pl.units);
+    p.scale_log2 = static_cast<float>(std::fabs(static_cast<double>(scale)) * 1.4426950408889634);
+    p.negate = scale < 0.f;
+    const unsigned grid = static_cast<unsigned>(pl.units * num_kv_heads * pl.P);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (head_size == 64)
+        e = block_size == 16 ? pa::launch_format<64, 16>(p, kv_dtype, grid, st)
+                             : pa::launch_format<64, 32>(p, kv_dtype, grid, st);
+    else
+        e = block_size == 16 ? pa::launch_format<128, 16>(p, kv_dtype, grid, st)
+                             : pa::launch_format<128, 32>(p, kv_dtype, grid, st);
+    if (e == cudaSuccess && pl.P > 1) {
+        const unsigned merge = static_cast<unsigned>(
+            (static_cast<long long>(num_tokens) * num_heads + pa::kWarps - 1) / pa::kWarps);
+        e = head_size == 64
+                ? pa::launch_pdl(pa::pa_prefill_merge_kernel<64>, merge, pa::kThreads, 0, st, p,
+                                 block_size)
+                : pa::launch_pdl(pa::pa_prefill_merge_kernel<128>, merge, pa::kThreads, 0, st, p,
+                                 block_size);
+    }
+    if (e != cudaSuccess) return fail(PA_ERR_CUDA, "prefill launch: %s", cudaGetErrorString(e));
+    return PA_OK;
+}
