@@ -49,8 +49,8 @@
  * for each block and kv head (PA_KV_FP8_E4M3_BLOCK, PA_KV_INT8_BLOCK): k_scale
  * and v_scale are then fp32 arrays [num_blocks, num_kv_heads], a code c of
  * block b and kv head h standing for c * scale[b][h].  Block scales are finite
- * and not negative; for V, one outside [2^-100, 2^100] counts as the nearer
- * end.
+ * and not negative; when read, a V scale outside [2^-60, 2^40] counts as the
+ * nearer end (below, that changes a value by at most 4e-16).
  * Pointer alignment: out, query, key_cache, value_cache and workspace 16 bytes;
  * block_tables and seq_lens 4 bytes.
  * Supported shapes: head_size 64 or 128; block_size 16 or 32;
@@ -349,11 +349,12 @@ pa_status pa_decode_noalloc(void* out, const void* query, const void* key_cache,
  *               (PA_ERR_UNSUPPORTED).  By default keys are split only when the
  *               batch has too few rows for every SM.
  * Values that a row does not see have no part in it, NaNs and infinities
- * included.  Everything else, the workspace (pa_prefill_workspace_size bytes;
- * its status word, and the partials of a split call after the header), the
- * device-side checks and the errors are as in pa_decode; a query_start outside
- * [0, num_tokens] or decreasing, or a length below n_s or above the block
- * table's, skips the sequence (PA_DEV_BAD_QUERY_START,
+ * included.  The workspace holds pa_prefill_workspace_size bytes: the header
+ * with the status word, then, for a split call, the decode's merge counts (not
+ * touched, so that one workspace serves both) and the partials.  Everything
+ * else, the device-side checks and the errors, is as in pa_decode; a
+ * query_start outside [0, num_tokens] or decreasing, or a length below n_s or
+ * above the block table's, skips the sequence (PA_DEV_BAD_QUERY_START,
  * PA_DEV_SEQ_LEN_OUT_OF_RANGE).
  */
 size_t pa_prefill_workspace_size(int num_tokens, int num_seqs, int num_heads, int num_kv_heads,

@@ -151,10 +151,12 @@ enum KvCodes : int {
     kInt8Block = 2    // int8, a scale per (block, kv head)
 };
 
-// A block's scale counts as within [2^-100, 2^100] (a scale of 0 stands for
-// zeros either way), so that log2 of it is finite and the running sums below
-// stay in fp32's range.
-constexpr float kScaleLog2Max = 100.f;
+// A block's V scale counts as within [2^-60, 2^40].  Within those 2^100 a
+// weight w = vs 2^(x - m) (see WarpAttn::page) of a token that matters to the
+// denominator, 2^-26 of the largest, is still a normal fp32 number, whatever
+// the other blocks' scales.  A smaller scale (a block of zeros has 2^-100, or
+// 0) changes a value by at most 448 2^-60 = 4e-16.
+constexpr float kScaleLog2Min = -60.f, kScaleLog2Max = 40.f;
 
 // The scales of the (up to two) pages of a stage: k multiplies the logits,
 // v_log2 is the base-2 logarithm of the V scale.
@@ -176,7 +178,7 @@ __device__ __forceinline__ PageScales load_page_scales(const float* k_scale, con
         const long long at = ok ? static_cast<long long>(ids[i]) * Hk + kvh : 0;
         ps.k[i] = ok ? __ldg(k_scale + at) : 0.f;
         const float v = ok ? log2f(__ldg(v_scale + at)) : 0.f;
-        ps.v_log2[i] = fminf(fmaxf(v, -kScaleLog2Max), kScaleLog2Max);
+        ps.v_log2[i] = fminf(fmaxf(v, kScaleLog2Min), kScaleLog2Max);
     }
     return ps;
 }

@@ -49,6 +49,9 @@ constexpr uint32_t kTmemColumns = 512;  // S of both tiles, then O of both
 constexpr float kLazyRescale = 8.f;     // log2 of the largest weight
 constexpr int kMaxSplits = 32;          // partials per row (merge_slots)
 constexpr unsigned long long kWaitNs = 2000000000ull;
+// The partials start behind the decode's merge counts, which have to stay 0
+// where calls of both share a workspace.
+constexpr size_t kBodyOffset = PA_WORKSPACE_HEADER_BYTES + PA_WORKSPACE_MERGE_COUNT_BYTES;
 
 enum Format : int { kFmtBf16 = 0, kFmtE4m3 = 1, kFmtE4m3Block = 2, kFmtInt8Block = 3 };
 
@@ -830,8 +833,9 @@ pa_status plan_prefill(PrefillPlan* pl, int num_tokens, int num_seqs, int num_he
     pl->tiles_per_part = static_cast<int>(per);
     pl->workspace_bytes = PA_WORKSPACE_HEADER_BYTES;
     if (P > 1) {
-        pl->workspace_bytes += static_cast<size_t>(num_tokens) * num_heads * P *
-                               (static_cast<size_t>(head_size) + 2) * sizeof(float);
+        pl->workspace_bytes = kBodyOffset + static_cast<size_t>(num_tokens) * num_heads * P *
+                                                (static_cast<size_t>(head_size) + 2) *
+                                                sizeof(float);
         pl->workspace_bytes = (pl->workspace_bytes + 255) & ~static_cast<size_t>(255);
     }
     return PA_OK;
@@ -919,7 +923,7 @@ extern "C" pa_status pa_prefill(void* out, const void* query, const void* key_ca
     p.query_start = query_start;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const size_t rows = static_cast<size_t>(num_tokens) * num_heads * pl.P;
-    p.ws_o = reinterpret_cast<float*>(ws + PA_WORKSPACE_HEADER_BYTES);
+    p.ws_o = reinterpret_cast<float*>(ws + pa::kBodyOffset);
     p.ws_m = p.ws_o + rows * head_size;
     p.ws_l = p.ws_m + rows;
     p.status = reinterpret_cast<uint32_t*>(ws);
