@@ -250,6 +250,14 @@ _ws_cache = {}
 _status_words = {}
 
 
+def _stream_ptr(stream, dev):
+    """The cudaStream_t of a call: the given stream's, or the current one's."""
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
 def workspace(nbytes: int, device, stream=None):
     """A zeroed workspace of at least nbytes on `device` for calls on `stream`
     (default: the current one), reused by the calls on that stream (its status
@@ -259,21 +267,24 @@ def workspace(nbytes: int, device, stream=None):
     zeroed by each replay."""
     import torch
     dev = torch.device(device)
+    if dev.index is None:
+        dev = torch.device(dev.type, torch.cuda.current_device())
+    nbytes = max(nbytes, WORKSPACE_HEADER_BYTES)
+    capturing = torch.cuda.is_current_stream_capturing()
+    key = (dev.index, _stream_ptr(stream, dev))
+    ws = _ws_cache.get(key)
+    if not capturing and ws is not None and ws.numel() >= nbytes:
+        return ws
     if stream is None:
         stream = torch.cuda.current_stream(dev)
-    nbytes = max(nbytes, WORKSPACE_HEADER_BYTES)
-    if torch.cuda.is_current_stream_capturing():
-        with torch.cuda.stream(stream):
-            return torch.zeros(nbytes, dtype=torch.uint8, device=dev)
-    key = (dev.type, dev.index, stream.cuda_stream)
-    ws = _ws_cache.get(key)
-    if ws is None or ws.numel() < nbytes:
-        with torch.cuda.stream(stream):  # zeroed, and later freed, in that stream's order
-            new = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
-            if ws is not None:  # keep the status bits
-                new[:4] = ws[:4]
-        ws = _ws_cache[key] = new
-    return ws
+    with torch.cuda.stream(stream):  # zeroed, and later freed, in that stream's order
+        new = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+        if capturing:
+            return new
+        if ws is not None:  # keep the status bits
+            new[:4] = ws[:4]
+    _ws_cache[key] = new
+    return new
 
 
 def _status_word(dev):
@@ -290,15 +301,19 @@ def _status_word(dev):
     return word
 
 
+_NO_CHANGE = contextlib.nullcontext()
+
+
 def _on_device(dev):
     """The library launches on the current device: make it `dev`."""
     import torch
     if torch.cuda.current_device() == dev.index:
-        return contextlib.nullcontext()
+        return _NO_CHANGE
     return torch.cuda.device(dev)
 
 
-def _ptr(t, name, dtypes=None, device=None):
+def _refuse(t, name, dtypes, device):
+    """Raise for what _ptr found wrong."""
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -308,11 +323,20 @@ def _ptr(t, name, dtypes=None, device=None):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if dtypes is not None and t.dtype not in dtypes:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
-    return t.data_ptr()
+    raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
 
 
+def _ptr(t, name, dtypes=None, device=None):
+    try:
+        if (t.is_cuda and (device is None or t.device == device) and t.is_contiguous()
+                and (dtypes is None or t.dtype in dtypes)):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _refuse(t, name, dtypes, device)
+
+
+@functools.lru_cache(maxsize=None)
 def _kv_types(code):
     import torch
     if code == PA_KV_BF16:
@@ -391,7 +415,6 @@ def decode(out, query, key_cache, value_cache, num_kv_heads: int, scale: float, 
         if alibi_slopes.shape != (Hq,):
             raise ValueError("alibi_slopes must be [num_heads]")
         alibi = _ptr(alibi_slopes, "alibi_slopes", (torch.float32,), dev)
-    st = stream if stream is not None else torch.cuda.current_stream(dev)
     # The library plans for, and launches on, the current device: make it the
     # tensors' device for the call.
     with _on_device(dev):
@@ -401,13 +424,13 @@ def decode(out, query, key_cache, value_cache, num_kv_heads: int, scale: float, 
                                    shared_prefix_blocks=shared_prefix_blocks,
                                    fp8_compute=bool(fp8_compute) and code == PA_KV_FP8_E4M3,
                                    schedule=schedule, stages=stages, num_sms=num_sms)
-            workspace_tensor = workspace(need, dev, st)
+            workspace_tensor = workspace(need, dev, stream)
         ws = _ptr(workspace_tensor, "workspace", None, dev)
         rc = lib().pa_decode_ex(*args_ptrs, S, Hq, int(num_kv_heads), D, float(scale), bt,
                                 block_tables.shape[1], sl, int(block_size), int(max_seq_len),
                                 int(num_blocks), code, ks, vs, ws,
                                 workspace_tensor.numel() * workspace_tensor.element_size(),
-                                st.cuda_stream,
+                                _stream_ptr(stream, dev),
                                 _opts(partition_pages, num_sms, stages, shared_prefix_blocks, alibi,
                                       fp8_compute, test_stall_copies, schedule, mha_cuda_cores))
     _check(rc)
@@ -453,18 +476,17 @@ def prefill(out, query, key_cache, value_cache, num_kv_heads: int, scale: float,
                          "query_start [num_seqs + 1]")
     S = seq_lens.shape[0]
     ks, vs = _scale_ptrs(code, k_scale, v_scale, num_blocks, num_kv_heads, dev)
-    st = stream if stream is not None else torch.cuda.current_stream(dev)
     with _on_device(dev):
         if workspace_tensor is None:  # (a given one is size-checked by the library)
             need = _prefill_workspace_size(dev.index, T, S, Hq, num_kv_heads, D, block_size,
                                            max_seq_len, code, partition_pages, num_sms)
-            workspace_tensor = workspace(need, dev, st)
+            workspace_tensor = workspace(need, dev, stream)
         rc = lib().pa_prefill(*ptrs, T, S, Hq, int(num_kv_heads), D, float(scale), bt,
                               block_tables.shape[1], sl, qs, int(block_size), int(max_seq_len),
                               num_blocks, code, ks, vs,
                               _ptr(workspace_tensor, "workspace", None, dev),
                               workspace_tensor.numel() * workspace_tensor.element_size(),
-                              st.cuda_stream, _opts(partition_pages, num_sms))
+                              _stream_ptr(stream, dev), _opts(partition_pages, num_sms))
     _check(rc)
     return out
 
@@ -508,7 +530,7 @@ def read_status(workspace_tensor=None, device=None, clear=False, stream=None) ->
         dev = torch.device(device) if device is not None else torch.device("cuda")
         if dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
-        words = [ws for key, ws in _ws_cache.items() if key[1] == dev.index]
+        words = [ws for key, ws in _ws_cache.items() if key[0] == dev.index]
         words += [w for index, w in _status_words.items() if index == dev.index]
         if words:  # calls of other streams may still be running
             torch.cuda.synchronize(dev)
@@ -630,24 +652,27 @@ def copy_blocks(key_cache, value_cache, src, dst, kv_dtype="bf16", status=None, 
 
 
 # ------------------------------------------------------------- appending tokens
-def _rows(t, name, heads, head_size, dev):
+def _rows(t, name, tokens, heads, head_size, dev):
     """Pointer and row stride of a bf16 [tokens, heads, head_size] tensor whose
     heads are dense (a view of a wider projection's output will do)."""
     import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected torch.bfloat16")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_size:
-        raise ValueError(f"{name} must be [num_tokens, {heads}, {head_size}]")
-    n, stride = t.shape[0], t.stride()
-    if n and (stride[2] != 1 or (heads > 1 and stride[1] != head_size)):
+    try:
+        if t.dtype != torch.bfloat16 or t.device != dev:
+            _refuse(t, name, (torch.bfloat16,), dev)
+    except AttributeError:
+        _refuse(t, name, None, dev)
+    if t.shape != (tokens, heads, head_size):
+        raise ValueError(f"{name} must be [{tokens}, {heads}, {head_size}]")
+    if tokens == 0:
+        return t.data_ptr(), 0
+    row, head, element = t.stride()
+    if element != 1 or (head != head_size and heads > 1):
         raise ValueError(f"{name}: a token's heads must be contiguous")
-    if n > 1 and stride[0] < heads * head_size:
+    if tokens == 1:
+        return t.data_ptr(), 0
+    if row < heads * head_size:
         raise ValueError(f"{name}: its rows overlap")
-    return t.data_ptr(), stride[0] if n > 1 else 0
+    return t.data_ptr(), row
 
 
 def append_kv(key_cache, value_cache, key, value, block_tables, seq_lens, block_size: int,
@@ -679,59 +704,60 @@ def append_kv(key_cache, value_cache, key, value, block_tables, seq_lens, block_
     code = kv_dtype_code(kv_dtype)
     dev = key_cache.device
     kv_types = _kv_types(code)
+    int32 = (torch.int32,)
     kc = _ptr(key_cache, "key_cache", kv_types, dev)
     vc = _ptr(value_cache, "value_cache", kv_types, dev)
     if key_cache.dim() != 5 or value_cache.dim() != 4:
         raise ValueError("key_cache must be 5-D and value_cache 4-D")
-    num_blocks, Hk, D = value_cache.shape[:3]
-    if value_cache.shape[3] != block_size \
-            or key_cache.shape != (num_blocks, Hk, D * key_cache.element_size() // 16, block_size,
-                                   16 // key_cache.element_size()):
+    num_blocks, Hk, D, B = value_cache.shape
+    x = 8 if code == PA_KV_BF16 else 16
+    if B != block_size or key_cache.shape != (num_blocks, Hk, D // x, B, x):
         raise ValueError("cache shapes do not match each other / block_size")
-    k, k_stride = _rows(key, "key", Hk, D, dev)
-    v, v_stride = _rows(value, "value", Hk, D, dev)
+    bt = _ptr(block_tables, "block_tables", int32, dev)
+    sl = _ptr(seq_lens, "seq_lens", int32, dev)
     T, S = key.shape[0], seq_lens.shape[0]
-    bt = _ptr(block_tables, "block_tables", (torch.int32,), dev)
-    sl = _ptr(seq_lens, "seq_lens", (torch.int32,), dev)
     if block_tables.dim() != 2 or block_tables.shape[0] != S or seq_lens.dim() != 1:
         raise ValueError("block_tables must be [num_seqs, max_blocks] and seq_lens [num_seqs]")
     qs = None
     if query_start is not None:
-        qs = _ptr(query_start, "query_start", (torch.int32,), dev)
+        qs = _ptr(query_start, "query_start", int32, dev)
         if query_start.shape != (S + 1,):
             raise ValueError("query_start must be [num_seqs + 1]")
-    if value.shape[0] != T or (qs is None and T != S):
-        raise ValueError("key and value need a row per token (per sequence without query_start)")
+    elif T != S:
+        raise ValueError("without query_start, key and value need a row per sequence")
+    k, k_stride = _rows(key, "key", T, Hk, D, dev)
+    v, v_stride = _rows(value, "value", T, Hk, D, dev)
     ks, vs = _scale_ptrs(code, k_scale, v_scale, num_blocks, Hk, dev)
-    o = AppendOptions(key_stride=k_stride, value_stride=v_stride)
+    table = pos = q = qo = None
+    max_position = rotary_dim = Hq = q_stride = qo_stride = 0
     if cos_sin is not None:
-        o.cos_sin = _ptr(cos_sin, "cos_sin", (torch.float32,), dev)
+        table = _ptr(cos_sin, "cos_sin", (torch.float32,), dev)
         if cos_sin.dim() != 2:
             raise ValueError("cos_sin must be [max_position, rotary_dim]")
-        o.max_position, o.rotary_dim = cos_sin.shape
-        o.interleaved = int(bool(interleaved))
+        max_position, rotary_dim = cos_sin.shape
         if positions is not None:
-            o.positions = _ptr(positions, "positions", (torch.int32,), dev)
+            pos = _ptr(positions, "positions", int32, dev)
             if positions.shape != (T,):
                 raise ValueError("positions must be [num_tokens]")
         if query is not None:
             if query_out is None:
                 query_out = query
-            o.num_heads = Hq = query.shape[1]
-            o.query, o.query_stride = _rows(query, "query", Hq, D, dev)
-            o.query_out, o.query_out_stride = _rows(query_out, "query_out", Hq, D, dev)
-            if query.shape[0] != T or query_out.shape[0] != T:
-                raise ValueError("query and query_out need a row per token")
+            if query.dim() != 3:
+                raise ValueError("query must be [num_tokens, num_heads, head_size]")
+            Hq = query.shape[1]
+            q, q_stride = _rows(query, "query", T, Hq, D, dev)
+            qo, qo_stride = _rows(query_out, "query_out", T, Hq, D, dev)
         elif query_out is not None:
             raise ValueError("query_out needs query")
     elif positions is not None or query is not None or query_out is not None or interleaved:
         raise ValueError("positions, query, query_out and interleaved need cos_sin")
-    st = stream if stream is not None else torch.cuda.current_stream(dev)
+    o = AppendOptions(k_stride, v_stride, table, max_position, rotary_dim, bool(interleaved), Hq,
+                      pos, q, qo, q_stride, qo_stride)
     with _on_device(dev):
         word = _status_word(dev) if status is None else status
-        rc = lib().pa_append_kv(kc, vc, k, v, T, S, Hk, D, bt, block_tables.shape[1], sl, qs,
-                                int(block_size), num_blocks, code, ks, vs,
+        rc = lib().pa_append_kv(kc, vc, k, v, T, S, Hk, D, bt, block_tables.shape[1], sl, qs, B,
+                                num_blocks, code, ks, vs,
                                 None if word is None else _ptr(word, "status", None, dev),
-                                st.cuda_stream, ctypes.byref(o))
+                                _stream_ptr(stream, dev), ctypes.byref(o))
     _check(rc)
     return query_out

@@ -5,12 +5,12 @@
 //   * task h < Hk: the new keys of kv head h in the block;
 //   * task Hk + h: its new values;
 //   * the tasks after them: the query rows of the block's new tokens.
-// A warp holds what it loads in registers (a whole page of new tokens is 4 KiB
-// at head size 128, 16 tokens), so every load is in flight before the first is
-// used, and a (block, head)'s largest |x| -- which fixes its scale -- needs one
-// warp reduction and no second pass over memory.  Warps share nothing and
-// never wait for one another: the rotation's table rows are re-read by each
-// head from L1, at twice the bytes of the bf16 rows they turn.
+// Warps share nothing and never wait for one another.  A warp takes a few rows
+// at a time in short loops -- what hides the loads' latency is many warps of
+// few registers, and straight-line code for a whole page of rows misses the
+// instruction cache (see append_keys).  A block whose scale is to be found is
+// read twice, the second time from L1; so are the rotation's table rows, by
+// each head.
 //
 // Bound: every row is read once and every element written once, so DRAM for
 // prompts; for single tokens the launch and two dependent rounds of loads
@@ -27,6 +27,13 @@ namespace pa {
 namespace {
 
 constexpr int kAppendWarps = 4;
+// CTAs per SM that the kernel's registers are held to (64 a thread: 32 warps).
+// Measured on 16 prompts of 18301 tokens, 64/8 heads, bf16, and on 12271 tokens
+// in chunks, 32/8 heads, int8 blocks of 32: 6 CTAs 132 and 69 us, 8 CTAs 125
+// and 64, 10 CTAs (which spill) 123 and 67.
+constexpr int kAppendCtasPerSm = 8;
+constexpr int kQueryRows = 32;  // rows of a query task (16: 131 us, 64: 126, of 125)
+constexpr int kStep = 16;  // slots of a V row that leave at once
 
 // Cache formats, as template argument.
 enum Format : int { kFmtBf16 = 0, kFmtE4m3 = 1, kFmtE4m3Block = 2, kFmtInt8Block = 3 };
@@ -51,25 +58,12 @@ struct AppendParams {
     int T, S, Hq, Hk, max_blocks;
     int max_position, rot, interleaved;
     int chunks;        // CTAs per unit (kAppendWarps tasks each)
+    int q_tokens, q_heads, q_groups;  // a query task: tokens, heads; head groups of a token
     int wide_v;        // value_cache is 32-byte aligned
 };
 
 __device__ __forceinline__ void flag(const AppendParams& p, uint32_t bits) {
     if (p.status) atomicOr(p.status, bits);
-}
-
-__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
-    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = bf16_lo(v[i]);
-        x[2 * i + 1] = bf16_hi(v[i]);
-    }
-}
-
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-    return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                      pack_bf16x2(x[6], x[7]));
 }
 
 // Which two 8-element chunks of a head's row lane-pair j of D / 16 owns, and
@@ -86,44 +80,83 @@ struct ChunkPair {
     }
 };
 
-// a' = a cos - b sin, b' = a sin + b cos: each product and each sum rounded
-// once in fp32 (no contraction), so that the result does not depend on how a
-// compiler fuses them -- it fixes the 8-bit codes and scales that follow.
-__device__ __forceinline__ void turn_pair(float& a, float& b, float c, float s) {
-    const float x = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
-    const float y = __fadd_rn(__fmul_rn(a, s), __fmul_rn(b, c));
-    a = x;
-    b = y;
+// Two fp32 products at once (a packed sum after them would be fused into an
+// fma, whatever its rounding modifier says; see Turn::two).
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
 }
 
-// The two chunks of one row at position `pos`, in fp32, turned.
-__device__ __forceinline__ void turned_chunks(const AppendParams& p, const ChunkPair& cp, int pos,
-                                              const uint4& wa, const uint4& wb, float (&xa)[8],
-                                              float (&xb)[8]) {
-    unpack8(wa, xa);
-    unpack8(wb, xb);
-    if (!cp.turn) return;
-    const float* cs = p.cos_sin + static_cast<long long>(pos) * p.rot;
-    const float* sn = cs + (p.rot >> 1);
-    const int i0 = p.interleaved ? 4 * cp.a : 8 * cp.a;  // first angles: of chunk a ...
-    const int i1 = p.interleaved ? 4 * cp.b : i0 + 4;    // ... and of b (or a's second half)
-    const float4 c0 = __ldg(reinterpret_cast<const float4*>(cs + i0));
-    const float4 c1 = __ldg(reinterpret_cast<const float4*>(cs + i1));
-    const float4 s0 = __ldg(reinterpret_cast<const float4*>(sn + i0));
-    const float4 s1 = __ldg(reinterpret_cast<const float4*>(sn + i1));
-    const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-    const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-    if (p.interleaved) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            turn_pair(xa[2 * i], xa[2 * i + 1], c[i], s[i]);
-            turn_pair(xb[2 * i], xb[2 * i + 1], c[4 + i], s[4 + i]);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) turn_pair(xa[i], xb[i], c[i], s[i]);
+// The cosines and sines that a chunk pair turns by at one position.
+struct Turn {
+    float2 c[4], s[4];
+    template <bool INTERLEAVED>
+    __device__ __forceinline__ void load(const AppendParams& p, const ChunkPair& cp, int pos) {
+        if (!cp.turn) return;
+        const float* cs = p.cos_sin + static_cast<long long>(pos) * p.rot;
+        const float* sn = cs + (p.rot >> 1);
+        const int i0 = INTERLEAVED ? 4 * cp.a : 8 * cp.a;  // first angles: of chunk a ...
+        const int i1 = INTERLEAVED ? 4 * cp.b : i0 + 4;    // ... and of b (or a's second half)
+        const float4 c0 = __ldg(reinterpret_cast<const float4*>(cs + i0));
+        const float4 c1 = __ldg(reinterpret_cast<const float4*>(cs + i1));
+        const float4 s0 = __ldg(reinterpret_cast<const float4*>(sn + i0));
+        const float4 s1 = __ldg(reinterpret_cast<const float4*>(sn + i1));
+        c[0] = make_float2(c0.x, c0.y);
+        c[1] = make_float2(c0.z, c0.w);
+        c[2] = make_float2(c1.x, c1.y);
+        c[3] = make_float2(c1.z, c1.w);
+        s[0] = make_float2(s0.x, s0.y);
+        s[1] = make_float2(s0.z, s0.w);
+        s[2] = make_float2(s1.x, s1.y);
+        s[3] = make_float2(s1.z, s1.w);
     }
-}
+    // a' = a cos - b sin, b' = a sin + b cos for two pairs: each product and
+    // each sum rounded once in fp32 (no contraction), so that the result does
+    // not depend on how a compiler fuses them -- it fixes the 8-bit codes and
+    // scales that follow.
+    __device__ __forceinline__ void two(float2& a, float2& b, int i) const {
+        const float2 ac = mul2(a, c[i]), bs = mul2(b, s[i]);
+        const float2 as = mul2(a, s[i]), bc = mul2(b, c[i]);
+        a = make_float2(__fsub_rn(ac.x, bs.x), __fsub_rn(ac.y, bs.y));
+        b = make_float2(__fadd_rn(as.x, bc.x), __fadd_rn(as.y, bc.y));
+    }
+};
+
+// A chunk pair in fp32, turned: element pairs x[0 .. 3] of chunk a, x[4 .. 7]
+// of chunk b.
+struct Chunks {
+    float2 x[8];
+    template <bool INTERLEAVED>
+    __device__ __forceinline__ void turned(const uint4& wa, const uint4& wb, const ChunkPair& cp,
+                                           const Turn& t) {
+        const uint32_t w[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = make_float2(bf16_lo(w[i]), bf16_hi(w[i]));
+        if (!cp.turn) return;
+        if constexpr (INTERLEAVED) {  // pairs are a word's halves, angle i for word i
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float2 a = make_float2(x[2 * i].x, x[2 * i + 1].x);
+                float2 b = make_float2(x[2 * i].y, x[2 * i + 1].y);
+                t.two(a, b, i);
+                x[2 * i] = make_float2(a.x, b.x);
+                x[2 * i + 1] = make_float2(a.y, b.y);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t.two(x[i], x[4 + i], i);
+        }
+    }
+    __device__ __forceinline__ uint4 bf16(int chunk) const {
+        const float2* y = x + 4 * chunk;
+        return make_uint4(pack_bf16x2(y[0].x, y[0].y), pack_bf16x2(y[1].x, y[1].y),
+                          pack_bf16x2(y[2].x, y[2].y), pack_bf16x2(y[3].x, y[3].y));
+    }
+};
 
 // A token's position, kept inside the table (flagged when it is not).
 __device__ __forceinline__ int position_of(const AppendParams& p, int row, int index) {
@@ -140,38 +173,61 @@ __device__ __forceinline__ constexpr float code_max() {
     return FMT == kFmtInt8Block ? 127.f : 448.f;
 }
 
-// x / scale, correctly rounded; for a power of two by its (exact) reciprocal.
+// x / scale for a power of two: by its reciprocal, exactly.
+struct PowerOfTwo {
+    float y;
+    __device__ __forceinline__ explicit PowerOfTwo(float scale) {
+        y = __uint_as_float((254u << 23) - __float_as_uint(scale));
+    }
+    static __device__ __forceinline__ bool is(float scale) {  // 2^-126 .. 2^126
+        const uint32_t b = __float_as_uint(scale);
+        return (b & 0x7fffffu) == 0 && b >= (1u << 23) && b <= (253u << 23);
+    }
+    __device__ __forceinline__ float operator()(float x) const { return x * y; }
+};
+
+// x / scale, correctly rounded, without a division per element: with y the
+// correctly rounded reciprocal, q = x y is off by an ulp at most, and
+// q + y (x - q scale), the remainder being exact in an fma, is the rounded
+// quotient (Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990).  Where q is not finite it stands.
 struct Divisor {
-    float s, inv;
-    bool pow2;
-    __device__ __forceinline__ explicit Divisor(float s_) {
-        s = s_;
-        const uint32_t b = __float_as_uint(s_);
-        const uint32_t e = b >> 23;  // (the sign counts: a negative scale is no power of two)
-        pow2 = (b & 0x7fffffu) == 0 && e >= 1 && e <= 253;
-        inv = pow2 ? __uint_as_float((254u - e) << 23) : 0.f;
+    float s, y;
+    __device__ __forceinline__ explicit Divisor(float scale) {
+        s = scale;
+        y = __frcp_rn(scale);
     }
     __device__ __forceinline__ float operator()(float x) const {
-        return pow2 ? x * inv : __fdiv_rn(x, s);
+        const float q = x * y;
+        const float r = fmaf(fmaf(-q, s, x), y, q);
+        return fabsf(q) < INFINITY ? r : q;
     }
 };
 
+// The nearest int8 code (ties to even), saturating at -127 and 127; a NaN
+// becomes 0.
+__device__ __forceinline__ uint32_t int8_code(float x) {
+    uint32_t r;
+    asm("{\n\t.reg .f32 t;\n\tmax.NaN.f32 t, %1, 0fC2FE0000;\n\t"  // -127
+        "cvt.rni.sat.s8.f32 %0, t;\n\t}"
+        : "=r"(r)
+        : "f"(x));
+    return r;
+}
+
 // Two values to two codes (nearest, ties to even, saturating; a NaN becomes
-// the e4m3 NaN, or int8 0), the first in the low byte.
+// the e4m3 NaN, or int8 0), the first in the low byte; the upper half is not
+// defined.
 template <int FMT>
 __device__ __forceinline__ uint32_t codes2(float x, float y) {
-    if constexpr (FMT == kFmtInt8Block) {
-        const int a = max(-127, min(127, __float2int_rn(x)));
-        const int b = max(-127, min(127, __float2int_rn(y)));
-        return (static_cast<uint32_t>(a) & 0xffu) | ((static_cast<uint32_t>(b) & 0xffu) << 8);
-    } else {
+    if constexpr (FMT == kFmtInt8Block)
+        return __byte_perm(int8_code(x), int8_code(y), 0x0040);
+    else
         return f32x2_to_e4m3x2(x, y);
-    }
 }
 template <int FMT>
-__device__ __forceinline__ uint32_t codes4(const Divisor& d, float x0, float x1, float x2,
-                                           float x3) {
-    return codes2<FMT>(d(x0), d(x1)) | (codes2<FMT>(d(x2), d(x3)) << 16);
+__device__ __forceinline__ uint32_t codes4(float x0, float x1, float x2, float x3) {
+    return __byte_perm(codes2<FMT>(x0, x1), codes2<FMT>(x2, x3), 0x5410);
 }
 
 // The smallest exponent e with amax <= code_max 2^e, within [-100, 100]:
@@ -184,13 +240,6 @@ __device__ __forceinline__ int scale_exponent(float amax) {
     const uint32_t m = b & 0x7fffffu;
     const int r = FMT == kFmtInt8Block ? e - 6 + (m > 0x7e0000u) : e - 8 + (m > 0x600000u);
     return max(-100, min(100, r));  // (0 and subnormals end at -100)
-}
-
-// The largest finite |x| (infinities saturate and NaNs stay NaN; neither may
-// push a neighbour's code to 0).
-__device__ __forceinline__ float amax_of(float amax, float x) {
-    const float a = fabsf(x);
-    return a <= 3.402823466e38f ? fmaxf(amax, a) : amax;
 }
 
 // The block's scale for a largest |x| of amax, joined with that of the tokens
@@ -216,12 +265,20 @@ __device__ __forceinline__ uint32_t rescaled(uint32_t w, float ratio) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             x[i] = static_cast<float>(static_cast<int8_t>((w >> (8 * i)) & 0xffu)) * ratio;
-        return codes2<FMT>(x[0], x[1]) | (codes2<FMT>(x[2], x[3]) << 16);
+        return codes4<FMT>(x[0], x[1], x[2], x[3]);
     } else {
         const uint32_t lo = e4m3_lo_pair(w), hi = e4m3_hi_pair(w);
-        return codes2<FMT>(f16_lo(lo) * ratio, f16_hi(lo) * ratio) |
-               (codes2<FMT>(f16_lo(hi) * ratio, f16_hi(hi) * ratio) << 16);
+        return codes4<FMT>(f16_lo(lo) * ratio, f16_hi(lo) * ratio, f16_lo(hi) * ratio,
+                           f16_hi(hi) * ratio);
     }
+}
+
+constexpr float kFltMax = 3.402823466e38f;
+
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
+    return x;
 }
 
 // 32 bytes to consecutive addresses: one store where the cache's base allows
@@ -249,42 +306,47 @@ struct Run {
 // Lane: chunk pair j = lane % (D / 16) of tokens lane / (D / 16) + TPI i.  A
 // key's 16-byte chunks of one column group are contiguous over tokens, so a
 // store instruction covers whole sectors of several groups.
-template <int D, int B, int FMT>
+template <int D, int B, int FMT, bool INTERLEAVED>
 __device__ __forceinline__ void append_keys(const AppendParams& p, const Run& r, int h,
                                             long long pb, int lane) {
-    constexpr int PJ = D / 16, TPI = 32 / PJ, IT = B / TPI;
+    constexpr int PJ = D / 16, TPI = 32 / PJ;
     constexpr bool BLOCK = FMT == kFmtE4m3Block || FMT == kFmtInt8Block;
     constexpr int PAGE = D * B * (FMT == kFmtBf16 ? 2 : 1);
     uint8_t* page = p.kc + (static_cast<size_t>(pb) * p.Hk + h) * PAGE;
     const ChunkPair cp(lane % PJ, p.rot);
-    const int tok0 = lane / PJ;
-    uint4 wa[IT], wb[IT];
-    int pos[IT];
-#pragma unroll
-    for (int i = 0; i < IT; ++i) {
-        const int t = tok0 + i * TPI - r.off;  // token of the run, if in [0, m)
-        wa[i] = wb[i] = make_uint4(0, 0, 0, 0);
-        pos[i] = 0;
-        if (t < 0 || t >= r.m) continue;
+    // Token t of the run: its chunks, turned.
+    auto token = [&](int t, Chunks& x, uint4& wa, uint4& wb) {
         const uint16_t* src = p.k + static_cast<long long>(r.row0 + t) * p.k_stride + h * D;
-        wa[i] = __ldg(reinterpret_cast<const uint4*>(src + 8 * cp.a));
-        wb[i] = __ldg(reinterpret_cast<const uint4*>(src + 8 * cp.b));
-        pos[i] = position_of(p, r.row0 + t, r.index0 + t);
-    }
+        wa = __ldg(reinterpret_cast<const uint4*>(src + 8 * cp.a));
+        wb = __ldg(reinterpret_cast<const uint4*>(src + 8 * cp.b));
+        Turn turn;
+        turn.load<INTERLEAVED>(p, cp, position_of(p, r.row0 + t, r.index0 + t));
+        x.turned<INTERLEAVED>(wa, wb, cp, turn);
+    };
+    Chunks x;
+    uint4 wa, wb;
     float scale = 1.f;
     if constexpr (BLOCK) {
-        float amax = 0.f;
+        // The largest finite |x|: infinities saturate and NaNs stay NaN, and
+        // neither may push a neighbour's code to 0.  (fmaxf drops NaNs; an
+        // infinity is seen at the end, and then left out.)
+        auto amax_below = [&](float limit) {
+            float amax = 0.f;
+#pragma unroll 1
+            for (int t = lane / PJ; t < r.m; t += TPI) {
+                token(t, x, wa, wb);
 #pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            const int t = tok0 + i * TPI - r.off;
-            if (t < 0 || t >= r.m) continue;
-            float xa[8], xb[8];
-            turned_chunks(p, cp, pos[i], wa[i], wb[i], xa, xb);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) amax = amax_of(amax_of(amax, xa[e]), xb[e]);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
+                for (int e = 0; e < 8; ++e) {
+                    const float u = fabsf(x.x[e].x), v = fabsf(x.x[e].y);
+                    amax = fmaxf(amax, u <= limit ? u : 0.f);
+                    amax = fmaxf(amax, v <= limit ? v : 0.f);
+                }
+            }
+            __syncwarp();
+            return warp_max(amax);
+        };
+        float amax = amax_below(INFINITY);
+        if (amax == INFINITY) amax = amax_below(kFltMax);
         float* at = p.k_scale + pb * p.Hk + h;
         float old;
         scale = block_scale<FMT>(at, r.off > 0, amax, &old);
@@ -292,50 +354,50 @@ __device__ __forceinline__ void append_keys(const AppendParams& p, const Run& r,
         if (lane == 0) *at = scale;
         if (scale > old) {  // the block's earlier tokens, in the new scale
             const float ratio = __fdiv_rn(old, scale);
-            uint4* words = reinterpret_cast<uint4*>(page);
-            for (int w = lane; w < PAGE / 16; w += 32) {
-                if (w % B >= r.off) continue;
-                uint4 v = words[w];
-                v.x = rescaled<FMT>(v.x, ratio);
-                v.y = rescaled<FMT>(v.y, ratio);
-                v.z = rescaled<FMT>(v.z, ratio);
-                v.w = rescaled<FMT>(v.w, ratio);
-                words[w] = v;
-            }
+            uint32_t* words = reinterpret_cast<uint32_t*>(page);
+#pragma unroll 1
+            for (int w = lane; w < PAGE / 4; w += 32)
+                if (w / 4 % B < r.off) words[w] = rescaled<FMT>(words[w], ratio);
         }
     } else if constexpr (FMT == kFmtE4m3) {
         scale = __ldg(p.k_scale);
     }
-    const Divisor div(scale);
-#pragma unroll
-    for (int i = 0; i < IT; ++i) {
-        const int tok = tok0 + i * TPI;
-        const int t = tok - r.off;
-        if (t < 0 || t >= r.m) continue;
-        float xa[8], xb[8];
-        turned_chunks(p, cp, pos[i], wa[i], wb[i], xa, xb);
-        if constexpr (FMT == kFmtBf16) {
-            uint4* dst = reinterpret_cast<uint4*>(page);
-            dst[cp.a * B + tok] = cp.turn ? pack8(xa) : wa[i];
-            dst[cp.b * B + tok] = cp.turn ? pack8(xb) : wb[i];
-        } else {
-            uint8_t* da = page + ((cp.a >> 1) * B + tok) * 16 + (cp.a & 1) * 8;
-            uint8_t* db = page + ((cp.b >> 1) * B + tok) * 16 + (cp.b & 1) * 8;
-            *reinterpret_cast<uint2*>(da) =
-                make_uint2(codes4<FMT>(div, xa[0], xa[1], xa[2], xa[3]),
-                           codes4<FMT>(div, xa[4], xa[5], xa[6], xa[7]));
-            *reinterpret_cast<uint2*>(db) =
-                make_uint2(codes4<FMT>(div, xb[0], xb[1], xb[2], xb[3]),
-                           codes4<FMT>(div, xb[4], xb[5], xb[6], xb[7]));
+    auto store = [&](const auto& div) {
+#pragma unroll 1
+        for (int t = lane / PJ; t < r.m; t += TPI) {
+            const int tok = r.off + t;
+            token(t, x, wa, wb);
+            if constexpr (FMT == kFmtBf16) {
+                uint4* dst = reinterpret_cast<uint4*>(page);
+                dst[cp.a * B + tok] = cp.turn ? x.bf16(0) : wa;
+                dst[cp.b * B + tok] = cp.turn ? x.bf16(1) : wb;
+            } else {
+                auto eight = [&](const float2* y) {
+                    return make_uint2(
+                        codes4<FMT>(div(y[0].x), div(y[0].y), div(y[1].x), div(y[1].y)),
+                        codes4<FMT>(div(y[2].x), div(y[2].y), div(y[3].x), div(y[3].y)));
+                };
+                uint8_t* da = page + ((cp.a >> 1) * B + tok) * 16 + (cp.a & 1) * 8;
+                uint8_t* db = page + ((cp.b >> 1) * B + tok) * 16 + (cp.b & 1) * 8;
+                *reinterpret_cast<uint2*>(da) = eight(x.x);
+                *reinterpret_cast<uint2*>(db) = eight(x.x + 4);
+            }
         }
-    }
+    };
+    if constexpr (FMT == kFmtBf16)
+        store(0);
+    else if (PowerOfTwo::is(scale))
+        store(PowerOfTwo(scale));
+    else
+        store(Divisor(scale));
 }
 
 // ---------------------------------------------------------------------- values
 // A V page holds a row of B tokens per head dim: lane l owns dims DV l ..
-// DV l + DV - 1 of every token (DV = D / 32), so the transposition happens in
-// its registers and each of its rows leaves in pieces as wide as the run
-// fills: 32 or 16 bytes, else single words or elements.
+// DV l + DV - 1 of every token (DV = D / 32).  Where the run fills 16 slots the
+// transposition happens in the lane's registers and each of its rows leaves as
+// one piece (32 bytes of bf16, 16 of codes); at the run's ends, and for single
+// tokens, elements are stored one by one.
 template <int D, int B, int FMT>
 __device__ __forceinline__ void append_values(const AppendParams& p, const Run& r, int h,
                                               long long pb, int lane) {
@@ -345,157 +407,143 @@ __device__ __forceinline__ void append_values(const AppendParams& p, const Run& 
     constexpr int PAGE = D * B * ELEM;
     uint8_t* rows = p.vc + (static_cast<size_t>(pb) * p.Hk + h) * PAGE +
                     static_cast<size_t>(lane) * DV * B * ELEM;
-    const int end = r.off + r.m;
-    uint32_t w[B][NW];
-    const uint16_t* src =
-        p.v + static_cast<long long>(r.row0 - r.off) * p.v_stride + h * D + DV * lane;
-#pragma unroll
-    for (int t = 0; t < B; ++t) {
-        const bool in = t >= r.off && t < end;
+    const uint16_t* src = p.v + static_cast<long long>(r.row0) * p.v_stride + h * D + DV * lane;
+    auto load = [&](int t, uint32_t (&w)[NW]) {  // token t of the run
         const uint16_t* at = src + static_cast<long long>(t) * p.v_stride;
         if constexpr (NW == 2) {
-            const uint2 v = in ? __ldg(reinterpret_cast<const uint2*>(at)) : make_uint2(0, 0);
-            w[t][0] = v.x;
-            w[t][1] = v.y;
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(at));
+            w[0] = v.x;
+            w[1] = v.y;
         } else {
-            w[t][0] = in ? __ldg(reinterpret_cast<const uint32_t*>(at)) : 0u;
+            w[0] = __ldg(reinterpret_cast<const uint32_t*>(at));
         }
-    }
-    if constexpr (FMT == kFmtBf16) {
+    };
+    auto value = [&](const uint32_t (&w)[NW], int d) {
+        return d % 2 ? bf16_hi(w[d / 2]) : bf16_lo(w[d / 2]);
+    };
+    float scale = 1.f;
+    if constexpr (BLOCK) {
+        // The largest finite |x|, as for the keys, on pairs of bf16 magnitudes
+        // (which order like integers); those above `limit` are left out.
+        auto amax_below = [&](uint32_t limit) {
+            uint32_t amax = 0;
+#pragma unroll 8
+            for (int t = 0; t < r.m; ++t) {
+                uint32_t w[NW];
+                load(t, w);
 #pragma unroll
-        for (int d = 0; d < DV; ++d) {
-            uint8_t* row = rows + d * B * 2;
-            // Words of two tokens' elements of this dim.
-            uint32_t x[B / 2];
-#pragma unroll
-            for (int t = 0; t < B / 2; ++t)
-                x[t] = __byte_perm(w[2 * t][d / 2], w[2 * t + 1][d / 2], d % 2 ? 0x7632 : 0x5410);
-#pragma unroll
-            for (int s = 0; s < B / 16; ++s) {  // 16 tokens, one 32-byte sector
-                if (r.off <= 16 * s && end >= 16 * s + 16) {
-                    const uint32_t v[8] = {x[8 * s],     x[8 * s + 1], x[8 * s + 2], x[8 * s + 3],
-                                           x[8 * s + 4], x[8 * s + 5], x[8 * s + 6], x[8 * s + 7]};
-                    store32(row + 32 * s, v, p.wide_v != 0);
-                    continue;
-                }
-#pragma unroll
-                for (int t = 8 * s; t < 8 * s + 8; ++t) {
-                    const bool lo = 2 * t >= r.off && 2 * t < end;
-                    const bool hi = 2 * t + 1 >= r.off && 2 * t + 1 < end;
-                    if (lo && hi) {
-                        *reinterpret_cast<uint32_t*>(row + 4 * t) = x[t];
-                    } else if (lo) {
-                        *reinterpret_cast<uint16_t*>(row + 4 * t) = static_cast<uint16_t>(x[t]);
-                    } else if (hi) {
-                        *reinterpret_cast<uint16_t*>(row + 4 * t + 2) =
-                            static_cast<uint16_t>(x[t] >> 16);
-                    }
+                for (int i = 0; i < NW; ++i) {
+                    const uint32_t m = w[i] & 0x7fff7fffu;
+                    amax = __vmaxu2(amax, limit == kFull ? m : m & __vcmpleu2(m, limit));
                 }
             }
-        }
-        return;
-    } else {
-        auto value = [&](int t, int d) {
-            return d % 2 ? bf16_hi(w[t][d / 2]) : bf16_lo(w[t][d / 2]);
+            amax = max(amax & 0xffffu, amax >> 16);
+            return __reduce_max_sync(kFull, amax);
         };
-        float scale;
-        if constexpr (BLOCK) {
-            float amax = 0.f;  // (rows outside the run are zeros)
-#pragma unroll
-            for (int t = 0; t < B; ++t)
-#pragma unroll
-                for (int d = 0; d < DV; ++d) amax = amax_of(amax, value(t, d));
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
-            float* at = p.v_scale + pb * p.Hk + h;
-            float old;
-            scale = block_scale<FMT>(at, r.off > 0, amax, &old);
-            __syncwarp();  // every lane has read the old scale
-            if (lane == 0) *at = scale;
-            if (scale > old) {
-                // The block's earlier tokens, in the new scale; the bytes behind
-                // them in a word are written back as they were.
-                const float ratio = __fdiv_rn(old, scale);
-                for (int i = 0; i < DV * (B / 4); ++i) {
-                    const int left = r.off - 4 * (i % (B / 4));  // earlier tokens in this word
-                    if (left <= 0) continue;
-                    uint32_t* at4 = reinterpret_cast<uint32_t*>(rows) + i;
-                    const uint32_t v = *at4, n = rescaled<FMT>(v, ratio);
-                    const uint32_t keep = left >= 4 ? 0u : kFull << (8 * left);
-                    *at4 = (n & ~keep) | (v & keep);
-                }
-            }
-        } else {
-            scale = __ldg(p.v_scale);
-        }
-        const Divisor div(scale);
-#pragma unroll
-        for (int d = 0; d < DV; ++d) {
-            uint8_t* row = rows + d * B;
-            uint32_t x[B / 4];
-#pragma unroll
-            for (int t = 0; t < B / 4; ++t)
-                x[t] = codes4<FMT>(div, value(4 * t, d), value(4 * t + 1, d),
-                                   value(4 * t + 2, d), value(4 * t + 3, d));
-#pragma unroll
-            for (int s = 0; s < B / 16; ++s) {
-                if (r.off <= 16 * s && end >= 16 * s + 16) {
-                    *reinterpret_cast<uint4*>(row + 16 * s) =
-                        make_uint4(x[4 * s], x[4 * s + 1], x[4 * s + 2], x[4 * s + 3]);
-                    continue;
-                }
-#pragma unroll
-                for (int t = 4 * s; t < 4 * s + 4; ++t) {
-                    if (r.off <= 4 * t && end >= 4 * t + 4) {
-                        *reinterpret_cast<uint32_t*>(row + 4 * t) = x[t];
-                        continue;
-                    }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (4 * t + e >= r.off && 4 * t + e < end)
-                            row[4 * t + e] = static_cast<uint8_t>(x[t] >> (8 * e));
-                }
+        uint32_t bits = amax_below(kFull);
+        if (bits >= 0x7f80u) bits = amax_below(0x7f7f7f7fu);
+        const float amax = __uint_as_float(bits << 16);
+        float* at = p.v_scale + pb * p.Hk + h;
+        float old;
+        scale = block_scale<FMT>(at, r.off > 0, amax, &old);
+        __syncwarp();  // every lane has read the old scale
+        if (lane == 0) *at = scale;
+        if (scale > old) {
+            // The block's earlier tokens, in the new scale; the bytes behind
+            // them in a word are written back as they were.
+            const float ratio = __fdiv_rn(old, scale);
+#pragma unroll 1
+            for (int i = 0; i < DV * (B / 4); ++i) {
+                const int left = r.off - 4 * (i % (B / 4));  // earlier tokens in this word
+                if (left <= 0) continue;
+                uint32_t* at4 = reinterpret_cast<uint32_t*>(rows) + i;
+                const uint32_t v = *at4, n = rescaled<FMT>(v, ratio);
+                const uint32_t keep = left >= 4 ? 0u : kFull << (8 * left);
+                *at4 = (n & ~keep) | (v & keep);
             }
         }
+    } else if constexpr (FMT == kFmtE4m3) {
+        scale = __ldg(p.v_scale);
     }
+    const int end = r.off + r.m;
+    auto store = [&](const auto& div) {
+#pragma unroll 1
+        for (int t0 = 0; t0 < B; t0 += kStep) {  // slots t0 .. t0 + 15
+            uint8_t* out = rows + t0 * ELEM;
+            if (r.off > t0 || end < t0 + kStep) {
+#pragma unroll 1
+                for (int t = max(t0, r.off); t < min(t0 + kStep, end); ++t) {
+                    uint32_t w[NW];
+                    load(t - r.off, w);
+#pragma unroll
+                    for (int d = 0; d < DV; ++d) {
+                        uint8_t* at = rows + (d * B + t) * ELEM;
+                        if constexpr (FMT == kFmtBf16)
+                            *reinterpret_cast<uint16_t*>(at) =
+                                static_cast<uint16_t>(w[d / 2] >> (16 * (d % 2)));
+                        else
+                            *at = static_cast<uint8_t>(codes2<FMT>(div(value(w, d)), 0.f));
+                    }
+                }
+                continue;
+            }
+            uint32_t w[kStep][NW];
+#pragma unroll
+            for (int i = 0; i < kStep; ++i) load(t0 + i - r.off, w[i]);
+#pragma unroll
+            for (int d = 0; d < DV; ++d) {
+                if constexpr (FMT == kFmtBf16) {
+                    uint32_t x[8];  // words of two tokens' elements of this dim
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        x[i] = __byte_perm(w[2 * i][d / 2], w[2 * i + 1][d / 2],
+                                           d % 2 ? 0x7632 : 0x5410);
+                    store32(out + d * B * 2, x, p.wide_v != 0);
+                } else {
+                    uint32_t x[4];  // words of four tokens' codes of this dim
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        x[i] = codes4<FMT>(div(value(w[4 * i], d)), div(value(w[4 * i + 1], d)),
+                                           div(value(w[4 * i + 2], d)), div(value(w[4 * i + 3], d)));
+                    *reinterpret_cast<uint4*>(out + d * B) = make_uint4(x[0], x[1], x[2], x[3]);
+                }
+            }
+        }
+    };
+    if constexpr (FMT == kFmtBf16)
+        store(0);
+    else if (PowerOfTwo::is(scale))
+        store(PowerOfTwo(scale));
+    else
+        store(Divisor(scale));
 }
 
 // --------------------------------------------------------------------- queries
-// Query rows a task covers: 4 KiB of them.
-template <int D>
-constexpr int query_rows() {
-    return 2048 / D;
-}
-
-// Rows [first, first + query_rows) of the run's (token, head) rows, heads
-// fastest.  A lane reads both chunks of a pair before it writes them, so
-// query_out may be query itself.
-template <int D>
-__device__ __forceinline__ void append_queries(const AppendParams& p, const Run& r, int first,
+// Task: tokens [t0, t0 + q_tokens) of the run, heads [h0, h0 + q_heads).  A
+// token's angles are loaded once for all its heads.  A lane reads both chunks
+// of a pair before it writes them, so query_out may be query itself.
+template <int D, bool INTERLEAVED>
+__device__ __forceinline__ void append_queries(const AppendParams& p, const Run& r, int t0, int h0,
                                                int lane) {
-    constexpr int PJ = D / 16, TPI = 32 / PJ, IT = query_rows<D>() / TPI;
+    constexpr int PJ = D / 16, TPI = 32 / PJ;
     const ChunkPair cp(lane % PJ, p.rot);
-    uint4 wa[IT], wb[IT];
-#pragma unroll
-    for (int i = 0; i < IT; ++i) {
-        const int n = first + lane / PJ + i * TPI;
-        const int t = n / p.Hq, h = n - t * p.Hq;
-        wa[i] = wb[i] = make_uint4(0, 0, 0, 0);
-        if (t >= r.m) continue;
-        const uint16_t* src = p.q + static_cast<long long>(r.row0 + t) * p.q_stride + h * D;
-        wa[i] = *reinterpret_cast<const uint4*>(src + 8 * cp.a);
-        wb[i] = *reinterpret_cast<const uint4*>(src + 8 * cp.b);
-    }
-#pragma unroll
-    for (int i = 0; i < IT; ++i) {
-        const int n = first + lane / PJ + i * TPI;
-        const int t = n / p.Hq, h = n - t * p.Hq;
-        if (t >= r.m) continue;
-        float xa[8], xb[8];
-        turned_chunks(p, cp, position_of(p, r.row0 + t, r.index0 + t), wa[i], wb[i], xa, xb);
-        uint16_t* dst = p.q_out + static_cast<long long>(r.row0 + t) * p.qo_stride + h * D;
-        *reinterpret_cast<uint4*>(dst + 8 * cp.a) = cp.turn ? pack8(xa) : wa[i];
-        *reinterpret_cast<uint4*>(dst + 8 * cp.b) = cp.turn ? pack8(xb) : wb[i];
+    const int t1 = min(t0 + p.q_tokens, r.m), h1 = min(h0 + p.q_heads, p.Hq);
+#pragma unroll 1
+    for (int t = t0; t < t1; ++t) {
+        Turn turn;
+        turn.load<INTERLEAVED>(p, cp, position_of(p, r.row0 + t, r.index0 + t));
+        const uint16_t* src = p.q + static_cast<long long>(r.row0 + t) * p.q_stride;
+        uint16_t* dst = p.q_out + static_cast<long long>(r.row0 + t) * p.qo_stride;
+#pragma unroll 1
+        for (int h = h0 + lane / PJ; h < h1; h += TPI) {
+            const int a = h * D + 8 * cp.a, b = h * D + 8 * cp.b;
+            const uint4 wa = *reinterpret_cast<const uint4*>(src + a);
+            const uint4 wb = *reinterpret_cast<const uint4*>(src + b);
+            Chunks x;
+            x.turned<INTERLEAVED>(wa, wb, cp, turn);
+            *reinterpret_cast<uint4*>(dst + a) = cp.turn ? x.bf16(0) : wa;
+            *reinterpret_cast<uint4*>(dst + b) = cp.turn ? x.bf16(1) : wb;
+        }
     }
 }
 
@@ -505,8 +553,8 @@ __device__ __forceinline__ void append_queries(const AppendParams& p, const Run&
 // most), so a unit finds its sequence from query_start alone, by a 32-way
 // search; units past a sequence's blocks have nothing to do.  Without
 // query_start, unit u is sequence u and its one row.
-template <int D, int B, int FMT>
-__global__ void __launch_bounds__(kAppendWarps * 32) pa_append_kernel(const AppendParams p) {
+template <int D, int B, int FMT, bool INTERLEAVED>
+__global__ void __launch_bounds__(kAppendWarps * 32, kAppendCtasPerSm) pa_append_kernel(const AppendParams p) {
     grid_dep_wait();
     grid_dep_launch_dependents();
     const int lane = threadIdx.x & 31;
@@ -553,9 +601,10 @@ __global__ void __launch_bounds__(kAppendWarps * 32) pa_append_kernel(const Appe
     r.row0 = a + (r.index0 - start);
     if (task >= 2 * p.Hk) {
         if (!p.q) return;
-        const long long first = static_cast<long long>(task - 2 * p.Hk) * query_rows<D>();
-        if (first < static_cast<long long>(r.m) * p.Hq)
-            append_queries<D>(p, r, static_cast<int>(first), lane);
+        const int q_task = task - 2 * p.Hk;
+        const int t0 = q_task / p.q_groups * p.q_tokens;
+        if (t0 < r.m)
+            append_queries<D, INTERLEAVED>(p, r, t0, q_task % p.q_groups * p.q_heads, lane);
         return;
     }
     const int pb = __ldg(p.bt + static_cast<long long>(s) * p.max_blocks + blk);
@@ -564,25 +613,25 @@ __global__ void __launch_bounds__(kAppendWarps * 32) pa_append_kernel(const Appe
         return;
     }
     if (task < p.Hk)
-        append_keys<D, B, FMT>(p, r, task, pb, lane);
+        append_keys<D, B, FMT, INTERLEAVED>(p, r, task, pb, lane);
     else
         append_values<D, B, FMT>(p, r, task - p.Hk, pb, lane);
 }
 
+template <int D, int B, int FMT>
+cudaError_t launch_append(const AppendParams& p, unsigned grid, cudaStream_t st) {
+    return p.interleaved
+               ? launch_pdl(pa_append_kernel<D, B, FMT, true>, grid, kAppendWarps * 32, 0, st, p)
+               : launch_pdl(pa_append_kernel<D, B, FMT, false>, grid, kAppendWarps * 32, 0, st, p);
+}
+
 template <int D, int B>
-cudaError_t launch_format(const AppendParams& p, int fmt, unsigned grid, cudaStream_t st) {
-    constexpr unsigned kThreadsPerCta = kAppendWarps * 32;
-    switch (fmt) {
-        case kFmtBf16:
-            return launch_pdl(pa_append_kernel<D, B, kFmtBf16>, grid, kThreadsPerCta, 0, st, p);
-        case kFmtE4m3:
-            return launch_pdl(pa_append_kernel<D, B, kFmtE4m3>, grid, kThreadsPerCta, 0, st, p);
-        case kFmtE4m3Block:
-            return launch_pdl(pa_append_kernel<D, B, kFmtE4m3Block>, grid, kThreadsPerCta, 0, st,
-                              p);
-        default:
-            return launch_pdl(pa_append_kernel<D, B, kFmtInt8Block>, grid, kThreadsPerCta, 0, st,
-                              p);
+cudaError_t launch_format(const AppendParams& p, pa_kv_dtype t, unsigned grid, cudaStream_t st) {
+    switch (t) {
+        case PA_KV_BF16: return launch_append<D, B, kFmtBf16>(p, grid, st);
+        case PA_KV_FP8_E4M3: return launch_append<D, B, kFmtE4m3>(p, grid, st);
+        case PA_KV_FP8_E4M3_BLOCK: return launch_append<D, B, kFmtE4m3Block>(p, grid, st);
+        default: return launch_append<D, B, kFmtInt8Block>(p, grid, st);
     }
 }
 
@@ -677,9 +726,14 @@ extern "C" pa_status pa_append_kv(void* key_cache, void* value_cache, const void
     }
     const long long units = query_start ? num_tokens / block_size + 2ll * num_seqs : num_seqs;
     const long long tokens = query_start ? (num_tokens < block_size ? num_tokens : block_size) : 1;
-    const long long rows_per_task = 2048 / head_size;
-    const long long q_tasks =
-        o.query ? (tokens * o.num_heads + rows_per_task - 1) / rows_per_task : 0;
+    // Query tasks: about 32 rows of a page's tokens; in a decode step, where a
+    // row is waited for, no more than one pass of a warp.
+    const int rows_per_pass = 512 / head_size;
+    const int q_rows = query_start ? pa::kQueryRows : rows_per_pass;
+    const int q_heads = o.num_heads < q_rows ? o.num_heads : q_rows;
+    const int q_tokens = o.query && q_rows / o.num_heads > 1 ? q_rows / o.num_heads : 1;
+    const int q_groups = o.query ? (o.num_heads + q_heads - 1) / q_heads : 1;
+    const long long q_tasks = o.query ? (tokens + q_tokens - 1) / q_tokens * q_groups : 0;
     const long long tasks = 2ll * num_kv_heads + q_tasks;
     const long long chunks = (tasks + pa::kAppendWarps - 1) / pa::kAppendWarps;
     if (units > 0x7fffffffll || units * chunks > 0x7fffffffll)
@@ -714,20 +768,19 @@ extern "C" pa_status pa_append_kv(void* key_cache, void* value_cache, const void
     p.rot = o.cos_sin ? o.rotary_dim : 0;
     p.interleaved = o.interleaved;
     p.chunks = static_cast<int>(chunks);
+    p.q_tokens = q_tokens;
+    p.q_heads = q_heads;
+    p.q_groups = q_groups;
     p.wide_v = aligned(value_cache, 32);
-    const int fmt = kv_dtype == PA_KV_BF16             ? pa::kFmtBf16
-                    : kv_dtype == PA_KV_FP8_E4M3       ? pa::kFmtE4m3
-                    : kv_dtype == PA_KV_FP8_E4M3_BLOCK ? pa::kFmtE4m3Block
-                                                       : pa::kFmtInt8Block;
     const unsigned grid = static_cast<unsigned>(units * chunks);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (head_size == 64)
-        e = block_size == 16 ? pa::launch_format<64, 16>(p, fmt, grid, st)
-                             : pa::launch_format<64, 32>(p, fmt, grid, st);
+        e = block_size == 16 ? pa::launch_format<64, 16>(p, kv_dtype, grid, st)
+                             : pa::launch_format<64, 32>(p, kv_dtype, grid, st);
     else
-        e = block_size == 16 ? pa::launch_format<128, 16>(p, fmt, grid, st)
-                             : pa::launch_format<128, 32>(p, fmt, grid, st);
+        e = block_size == 16 ? pa::launch_format<128, 16>(p, kv_dtype, grid, st)
+                             : pa::launch_format<128, 32>(p, kv_dtype, grid, st);
     if (e != cudaSuccess) return fail(PA_ERR_CUDA, "append launch: %s", cudaGetErrorString(e));
     return PA_OK;
 }
