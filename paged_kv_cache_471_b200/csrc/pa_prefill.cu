@@ -5,12 +5,11 @@
 // One CTA per (group of query tokens, kv head, key partition).  Its rows are
 // (query token, head of the kv head's group) pairs, tokens slowest, in two
 // tiles of 128 rows; key tiles of 128 tokens pass by once for all 256 rows:
-//   * warps 8-11 gather the tile's pages into shared memory as tensor-core
-//     operands.  Both page layouts are K-major in 16-byte pieces already (K: 8
-//     head dims of a token, V: 8 tokens of a head dim), so a piece of a bf16
-//     page is one 16-byte asynchronous copy to its place; 8-bit codes are
-//     widened to f16 (exact) on the way;
-//   * warp 12 issues the products: S = Q K^T into TMEM, then O += P V with P
+//   * warps 8 and 9 gather the tile's pages into shared memory as tensor-core
+//     operands.  Both page layouts are K-major already (K: 16-byte columns of 8
+//     head dims; V: rows of B tokens), so bulk and TMA copies put bf16 pages in
+//     place without a register; 8-bit codes are widened to f16 (exact) on the way;
+//   * warp 10 issues the products: S = Q K^T into TMEM, then O += P V with P
 //     read from TMEM, where it lies over the S it came from;
 //   * warps 0-3 and 4-7 hold a row of one tile per thread: the running maximum
 //     and sum, P = 2^(x - m) back to TMEM.  While one tile is in softmax, the
@@ -21,12 +20,14 @@
 //
 // Bound: 4 D flops per (row, key) on the tensor cores, against one exponential
 // per (row, key): 16 a clock and SM, so at D = 128 both need the same time.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
+#include <mutex>
 
 #include "pa_launch.cuh"
 #include "pa_tcgen05.cuh"
@@ -41,14 +42,20 @@ constexpr int kKeys = 128;        // keys of a tile
 constexpr int kStages = 2;        // K tiles, and V tiles, in shared memory
 constexpr int kInfo = 4;          // key tiles whose page info is kept
 constexpr int kSoftmaxWarps = 8;
-constexpr int kLoadWarps = 4;
-constexpr int kLoadThreads = kLoadWarps * 32;
+constexpr int kLoadWarps = 2;
 constexpr int kMmaWarp = kSoftmaxWarps + kLoadWarps;
 constexpr int kCtaThreads = (kMmaWarp + 1) * 32;
 constexpr uint32_t kTmemColumns = 512;  // S of both tiles, then O of both
+#ifndef PA_SPLIT
+#define PA_SPLIT 2
+#endif
+// The weights of a tile go to the product in two parts, the first of
+// kFirstKeys keys, so that it begins before the last weight is there.
+constexpr int kFirstKeys = 32 * PA_SPLIT;
 constexpr float kLazyRescale = 8.f;     // log2 of the largest weight
 constexpr int kMaxSplits = 32;          // partials per row (merge_slots)
 constexpr unsigned long long kWaitNs = 2000000000ull;
+constexpr unsigned long long kDrainNs = 20000000ull;  // after a wait that ran out
 // The partials start behind the decode's merge counts, which have to stay 0
 // where calls of both share a workspace.
 constexpr size_t kBodyOffset = PA_WORKSPACE_HEADER_BYTES + PA_WORKSPACE_MERGE_COUNT_BYTES;
@@ -76,6 +83,13 @@ struct PrefillParams {
     int units;             // token groups (an upper bound)
     float scale_log2;      // |scale| log2(e)
     int negate;            // scale < 0: the queries are negated
+    int v_pages;           // num_blocks * Hk: pages of the tensor maps
+};
+
+// Tensor maps of the bf16 caches: K as rows of one page each, V as pages of D
+// rows of B tokens.
+struct PageMaps {
+    CUtensorMap k, v;
 };
 
 // The sequence of a row or unit: the largest s in [0, S) with first(s) <= x,
@@ -94,17 +108,23 @@ __device__ __forceinline__ int find_sequence(int S, int lane, First first, int x
     }
 }
 
-template <int D, int FMT>
+template <int D, int B, bool BF16>
 struct Layout {  // shared memory, in bytes
-    static constexpr int kTile = kRows * D * 2;  // a Q tile, a K tile or a V tile
+    static constexpr int kTile = kRows * D * 2;  // a Q tile or a K tile
+    // A V tile of bf16 pages: the pages as the TMA unit lays them down, rows of
+    // B tokens with the 32- or 64-byte swizzle.  Of 8-bit pages: 8 keys of every
+    // head dim, 16 bytes each, a step apart that is off the 128-byte period of
+    // the banks by as much as makes a warp's stores -- rows of V, 16-byte pieces
+    // fastest -- hit every bank once.
+    static constexpr int kVStep = D * 16 + (B == 16 ? 64 : 32);
+    static constexpr int kVTile = BF16 ? kTile : kKeys / 8 * kVStep;
     static constexpr int q = 0;
     static constexpr int k = q + kTiles * kTile;
     static constexpr int v = k + kStages * kTile;
-    static constexpr int info = v + kStages * kTile;          // per key tile: 32 floats
-    static constexpr int q_mul = info + kInfo * 32 * 4;       // per row: float
-    static constexpr int bad = q_mul + kTiles * kRows * 4;    // 8 words: see scrub
+    static constexpr int info = v + kStages * kVTile;         // per key tile: 32 floats
+    static constexpr int bad = info + kInfo * 32 * 4;         // 8 words: see scrub
     static constexpr int bars = bad + 32;
-    static constexpr int n_bars = 4 * kStages + 2 * kTiles + kInfo + 1;
+    static constexpr int n_bars = 5 * kStages + 3 * kTiles + kInfo + 2;
     static constexpr int tmem_slot = bars + 8 * n_bars;
     static constexpr int total = tmem_slot + 16;
 };
@@ -114,18 +134,19 @@ struct Layout {  // shared memory, in bytes
 // formats; 8 pages at most).
 constexpr int kInfoK = 8, kInfoV = 16;
 
-__device__ __forceinline__ bool finite_bf16(uint32_t bits) { return (bits & 0x7f80u) != 0x7f80u; }
+constexpr float kTinyFactor = 1e-30f;  // of a logit: what is below counts as it
 
 template <int D, int B, int FMT>
-__global__ void __launch_bounds__(kCtaThreads, 1) pa_prefill_kernel(const PrefillParams p) {
-    using L = Layout<D, FMT>;
+__global__ void __launch_bounds__(kCtaThreads, 1) pa_prefill_kernel(const PrefillParams p, const __grid_constant__ PageMaps maps) {
+    using L = Layout<D, B, FMT == kFmtBf16>;
     constexpr bool BF16 = FMT == kFmtBf16;
     constexpr bool BLOCK = FMT == kFmtE4m3Block || FMT == kFmtInt8Block;
     constexpr bool INT8 = FMT == kFmtInt8Block;
     constexpr int ELEM = BF16 ? 2 : 1;
     constexpr int PAGE = D * B * ELEM;
     constexpr int NPG = kKeys / B;  // pages of a key tile
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ __align__(1024) uint8_t prefill_smem[];
+    uint8_t* const smem = prefill_smem;
     grid_dep_wait();
     grid_dep_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -174,21 +195,26 @@ __global__ void __launch_bounds__(kCtaThreads, 1) pa_prefill_kernel(const Prefil
     const uint32_t bars = sbase + L::bars;
     const uint32_t k_full = bars, k_empty = k_full + 8 * kStages, v_full = k_empty + 8 * kStages,
                    v_empty = v_full + 8 * kStages, s_ready = v_empty + 8 * kStages,
-                   p_ready = s_ready + 8 * kTiles, i_full = p_ready + 8 * kTiles,
-                   drained = i_full + 8 * kInfo;
+                   p_first = s_ready + 8 * kTiles, p_ready = p_first + 8 * kTiles,
+                   i_full = p_ready + 8 * kTiles,
+                   q_full = i_full + 8 * kInfo, v_land = q_full + 8,
+                   drained = v_land + 8 * kStages;
     uint32_t* bad = reinterpret_cast<uint32_t*>(smem + L::bad);
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(k_full + 8 * i, kLoadThreads);
-            mbar_init(v_full + 8 * i, kLoadThreads);
+            mbar_init(k_full + 8 * i, BF16 ? 1 : 32);
+            mbar_init(v_full + 8 * i, BF16 ? 1 : 32);
+            mbar_init(v_land + 8 * i, 1);
             mbar_init(k_empty + 8 * i, 1);
             mbar_init(v_empty + 8 * i, 1);
         }
         for (int t = 0; t < kTiles; ++t) {
             mbar_init(s_ready + 8 * t, 1);
+            mbar_init(p_first + 8 * t, kRows);
             mbar_init(p_ready + 8 * t, kRows);
         }
         for (int i = 0; i < kInfo; ++i) mbar_init(i_full + 8 * i, 1);
+        mbar_init(q_full, kTiles * kRows);
         mbar_init(drained, 1);
         fence_mbar_init();
         for (int i = 0; i < 8; ++i) bad[i] = 0;
@@ -211,7 +237,6 @@ __global__ void __launch_bounds__(kCtaThreads, 1) pa_prefill_kernel(const Prefil
 
     if (warp >= kSoftmaxWarps && warp < kMmaWarp) {
         // ================================================ loaders
-        const int tid = threadIdx.x - kSoftmaxWarps * 32;
         const int32_t* btrow = p.bt + static_cast<long long>(s) * p.max_blocks;
         const size_t block_stride = static_cast<size_t>(p.Hk) * PAGE;
         const size_t head_off = static_cast<size_t>(kvh) * PAGE;
@@ -226,53 +251,6 @@ __global__ void __launch_bounds__(kCtaThreads, 1) pa_prefill_kernel(const Prefil
         };
         int next = page_id(0);
 
-        // The query rows: row r of a tile at 16 r of each 16-byte column, so
-        // that the tile is an operand.  f16 operands (8-bit caches) are scaled
-        // per row by a power of two, which puts the largest |q| in [2^14, 2^15).
-        for (int t = 0; t < kTiles; ++t) {
-            const int qt = tok0 + t * p.tokens_per_tile + tid / p.G;
-            const bool ok = tid < p.tokens_per_tile * p.G && qt < n;
-            const uint4* src = reinterpret_cast<const uint4*>(
-                p.q + ((static_cast<long long>(a) + (ok ? qt : 0)) * p.Hq +
-                       static_cast<long long>(kvh) * p.G + (ok ? tid % p.G : 0)) * D);
-            const uint32_t dst = sbase + L::q + t * L::kTile + tid * 16;
-            const uint32_t flip = p.negate ? 0x80008000u : 0u;
-            float up = 1.f;
-            if constexpr (!BF16) {
-                float amax = 0.f;
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c) {
-                    const uint4 w = ok ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-                    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(x[i])), fabsf(bf16_hi(x[i]))));
-                }
-                int e = 0;  // amax in [2^(14 + e), 2^(15 + e))
-                if (amax > 0.f && amax < INFINITY)
-                    e = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14;
-                e = max(-110, min(113, e));
-                up = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-                reinterpret_cast<float*>(smem + L::q_mul)[t * kRows + tid] =
-                    __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-            }
-#pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-                uint4 w = ok ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-                w.x ^= flip;
-                w.y ^= flip;
-                w.z ^= flip;
-                w.w ^= flip;
-                if constexpr (!BF16) {
-                    w.x = pack_f16x2(bf16_lo(w.x) * up, bf16_hi(w.x) * up);
-                    w.y = pack_f16x2(bf16_lo(w.y) * up, bf16_hi(w.y) * up);
-                    w.z = pack_f16x2(bf16_lo(w.z) * up, bf16_hi(w.z) * up);
-                    w.w = pack_f16x2(bf16_lo(w.w) * up, bf16_hi(w.w) * up);
-                }
-                sts128(dst + c * (kRows * 16), w);
-            }
-        }
-
         auto widen = [&](uint32_t w, uint32_t& lo, uint32_t& hi) {
             lo = INT8 ? int8_lo_pair(w) : e4m3_lo_pair(w);
             hi = INT8 ? int8_hi_pair(w) : e4m3_hi_pair(w);
@@ -286,168 +264,240 @@ __global__ void __launch_bounds__(kCtaThreads, 1) pa_prefill_kernel(const Prefil
             sts128(lo_at, x);
             sts128(hi_at, y);
         };
-
-        for (int j = 0; j < steps && !lost; ++j) {
-            const int st = j % kStages, round = j / kStages;
-            const int ids = next;
-            next = page_id(j + 1);
-            const int key0 = (j0 + j) * kKeys;
-            if (warp == kSoftmaxWarps) {
-                // Page info for the softmax warps (kInfo tiles deep: the slot's
-                // last user is done once K of tile j - 2 has been released).
-                float* info = reinterpret_cast<float*>(smem + L::info) + (j % kInfo) * 32;
-                if (!wait(k_empty + 8 * st, round + 1)) break;
-                const unsigned legal = __ballot_sync(kFull, lane < NPG && ids >= 0);
-                if (lane == 0) reinterpret_cast<uint32_t*>(info)[0] = legal;
-                if constexpr (BLOCK) {
-                    if (lane < NPG) {
-                        const PageScales ps = load_page_scales(p.k_scale, p.v_scale, ids, -1,
-                                                               p.num_blocks, p.Hk, kvh);
-                        info[kInfoK + lane] = ps.k[0];
-                        info[kInfoV + lane] = ps.v_log2[0];
-                    }
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(i_full + 8 * (j % kInfo));
+        // Values of keys that not every row sees, or none: non-finite ones are
+        // kept out of the product (0 times NaN is NaN), and noted where some row
+        // does see them.  For a 16-byte piece of one head dim from key `key` on:
+        // which of its elements those keys are (their top bits), ...
+        constexpr int kBits = ELEM * 8, kPer = 32 / kBits;
+        struct Late {
+            uint32_t top[4];
+        };
+        auto late_keys = [&](int key) {
+            Late m;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                m.top[i] = 0;
+#pragma unroll
+                for (int e = 0; e < kPer; ++e)
+                    if (key + i * kPer + e >= seen0) m.top[i] |= 1u << ((e + 1) * kBits - 1);
             }
-            const uint32_t kdst = sbase + L::k + st * L::kTile;
-            const uint32_t vdst = sbase + L::v + st * L::kTile;
-            // Tiles with keys that some row does not see: non-finite values of
-            // those are kept out of the product (0 times NaN is NaN) and noted
-            // for the rows that do see them.
-            const bool edge = key0 + kKeys > seen0;
-            auto scrub = [&](uint4& w, int key, int count_keys) {  // keys of one head dim, bf16
-                uint32_t x[4] = {w.x, w.y, w.z, w.w};
+            return m;
+        };
+        // ... which of them are not finite (an exponent, or a code, of all ones
+        // carries into the top bit), ...
+        auto odd_of = [&](uint32_t x, uint32_t top) -> uint32_t {
+            if constexpr (BF16) return ((x & 0x7f807f80u) + 0x00800080u) & top;
+            if constexpr (INT8) return 0u;
+            return ((x & 0x7f7f7f7fu) + 0x01010101u) & top;
+        };
+        auto odd_any = [&](const uint4& w, const Late& m) -> uint32_t {
+            return odd_of(w.x, m.top[0]) | odd_of(w.y, m.top[1]) | odd_of(w.z, m.top[2]) |
+                   odd_of(w.w, m.top[3]);
+        };
+        // ... and the piece without those.
+        auto scrub = [&](uint4& w, const Late& m, int key) {
+            uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll 1
+            for (int e = 0; e < 4 * kPer; ++e) {
+                const int i = e / kPer, k = key + e - seen0;
+                const uint32_t top = i == 0 ? m.top[0] : i == 1 ? m.top[1] : i == 2 ? m.top[2]
+                                                                                    : m.top[3];
+                const uint32_t v = i == 0 ? x[0] : i == 1 ? x[1] : i == 2 ? x[2] : x[3];
+                if (!((odd_of(v, top) >> ((e % kPer + 1) * kBits - 1)) & 1u)) continue;
+                const uint32_t keep = ~(((1u << kBits) - 1u) << (e % kPer * kBits));
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    if (e >= count_keys) break;
-                    const uint32_t v = (x[e / 2] >> (16 * (e % 2))) & 0xffffu;
-                    const bool hidden = key + e >= seen_end;
-                    if (key + e < seen0 || (finite_bf16(v) && !hidden)) continue;
-                    x[e / 2] &= e % 2 ? 0x0000ffffu : 0xffff0000u;
-                    if (!hidden) {
-                        const int i = key + e - seen0;
-                        atomicOr(bad + (i >> 5), 1u << (i & 31));
-                    }
-                }
-                w = make_uint4(x[0], x[1], x[2], x[3]);
-            };
-            auto scrub_codes = [&](uint32_t w, int key) {  // 4 keys of one head dim
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t v = (w >> (8 * e)) & 0x7fu;
-                    const bool hidden = key + e >= seen_end;
-                    if (key + e < seen0 || ((INT8 || v != 0x7fu) && !hidden)) continue;
-                    w &= ~(0xffu << (8 * e));
-                    if (!hidden) {
-                        const int i = key + e - seen0;
-                        atomicOr(bad + (i >> 5), 1u << (i & 31));
-                    }
-                }
-                return w;
-            };
-            if constexpr (BF16) {
-                // ---- K: pieces (column group c, token) of a page are contiguous
-                constexpr int KP = D / 8 * B;  // pieces of a page
-                if (!wait(k_empty + 8 * st, round + 1)) break;
-#pragma unroll 4
-                for (int i = tid; i < NPG * KP; i += kLoadThreads) {
-                    const int pg = i / KP, c = i % KP / B, tk = i % B;
-                    const int id = __shfl_sync(kFull, ids, pg);
-                    cp_async16(kdst + c * (kKeys * 16) + (pg * B + tk) * 16,
-                               p.kc + (id < 0 ? 0 : id) * block_stride + head_off + i % KP * 16,
-                               id < 0 ? 0u : 16u);
-                }
-                cp_async_commit();
-                if (j > 0) {  // V of the tile before has landed
-                    cp_async_wait<1>();
-                    fence_smem_to_async();
-                    mbar_arrive(v_full + 8 * ((j - 1) % kStages));
-                }
-                // ---- V: pieces (head dim, 8 tokens); a warp covers whole rows
-                constexpr int VR = B / 8, RW = 32 / VR;  // pieces of a row, rows per warp
-                constexpr int VP = D * VR;
-                if (!wait(v_empty + 8 * st, round + 1)) break;
-#pragma unroll 4
-                for (int i = tid; i < NPG * VP; i += kLoadThreads) {
-                    const int pg = i / VP, in_page = i % VP;
-                    const int d = in_page / 32 * RW + lane % RW, h = lane / RW;
-                    const int id = __shfl_sync(kFull, ids, pg);
-                    const uint8_t* src = p.vc + (id < 0 ? 0 : id) * block_stride + head_off +
-                                         (d * B + h * 8) * 2;
-                    const uint32_t dst = vdst + (pg * VR + h) * (D * 16) + d * 16;
-                    if (edge) {
-                        uint4 w = id < 0 ? make_uint4(0, 0, 0, 0)
-                                         : __ldg(reinterpret_cast<const uint4*>(src));
-                        scrub(w, key0 + pg * B + h * 8, 8);
-                        sts128(dst, w);
-                    } else {
-                        cp_async16(dst, src, id < 0 ? 0u : 16u);
-                    }
-                }
-                cp_async_commit();
-                cp_async_wait<1>();  // K has landed
-                fence_smem_to_async();
-                mbar_arrive(k_full + 8 * st);
-            } else {
-                // ---- K: pieces (16 head dims, token); V: pieces (head dim, 16 tokens)
-                constexpr int KP = D / 16 * B, VR = B / 16, VP = D * VR;
-                constexpr int IT = NPG * KP / kLoadThreads;  // pieces per thread
-                static_assert(NPG * KP == NPG * VP && NPG * KP % kLoadThreads == 0, "");
-                uint4 w[IT];
-#pragma unroll
-                for (int k = 0; k < IT; ++k) {
-                    const int i = tid + k * kLoadThreads, pg = i / KP;
-                    const int id = __shfl_sync(kFull, ids, pg);
-                    w[k] = id < 0 ? make_uint4(0, 0, 0, 0)
-                                  : __ldg(reinterpret_cast<const uint4*>(
-                                        p.kc + id * block_stride + head_off + i % KP * 16));
-                }
-                if (!wait(k_empty + 8 * st, round + 1)) break;
-#pragma unroll
-                for (int k = 0; k < IT; ++k) {
-                    const int i = tid + k * kLoadThreads;
-                    const int pg = i / KP, c = i % KP / B, tk = i % B;
-                    const uint32_t at = kdst + 2 * c * (kKeys * 16) + (pg * B + tk) * 16;
-                    put16(at, at + kKeys * 16, w[k]);
-                }
-                fence_smem_to_async();
-                mbar_arrive(k_full + 8 * st);
-#pragma unroll
-                for (int k = 0; k < IT; ++k) {
-                    const int i = tid + k * kLoadThreads, pg = i / VP;
-                    const int d = VR == 1 ? i % VP : i % VP / 32 * 16 + lane % 16;
-                    const int h = VR == 1 ? 0 : lane / 16;
-                    const int id = __shfl_sync(kFull, ids, pg);
-                    w[k] = id < 0 ? make_uint4(0, 0, 0, 0)
-                                  : __ldg(reinterpret_cast<const uint4*>(
-                                        p.vc + id * block_stride + head_off + d * B + h * 16));
-                    if (edge) {
-                        const int key = key0 + pg * B + h * 16;
-                        w[k].x = scrub_codes(w[k].x, key);
-                        w[k].y = scrub_codes(w[k].y, key + 4);
-                        w[k].z = scrub_codes(w[k].z, key + 8);
-                        w[k].w = scrub_codes(w[k].w, key + 12);
-                    }
-                }
-                if (!wait(v_empty + 8 * st, round + 1)) break;
-#pragma unroll
-                for (int k = 0; k < IT; ++k) {
-                    const int i = tid + k * kLoadThreads, pg = i / VP;
-                    const int d = VR == 1 ? i % VP : i % VP / 32 * 16 + lane % 16;
-                    const int h = VR == 1 ? 0 : lane / 16;
-                    const uint32_t at = vdst + 2 * (pg * VR + h) * (D * 16) + d * 16;
-                    put16(at, at + D * 16, w[k]);
-                }
-                fence_smem_to_async();
-                mbar_arrive(v_full + 8 * st);
+                for (int u = 0; u < 4; ++u) x[u] &= u == i ? keep : kFull;
+                if (key + e < seen_end) atomicOr(bad + (k >> 5), 1u << (k & 31));
             }
-        }
+            w = make_uint4(x[0], x[1], x[2], x[3]);
+        };
+        auto page_info = [&](int j, int ids) {
+            // (kInfo tiles deep: the slot's last user is done once K of tile
+            // j - 2 has been released.)
+            float* info = reinterpret_cast<float*>(smem + L::info) + (j % kInfo) * 32;
+            const unsigned legal = __ballot_sync(kFull, lane < NPG && ids >= 0);
+            if (lane == 0) reinterpret_cast<uint32_t*>(info)[0] = legal;
+            if constexpr (BLOCK) {
+                if (lane < NPG) {
+                    const PageScales ps = load_page_scales(p.k_scale, p.v_scale, ids, -1,
+                                                           p.num_blocks, p.Hk, kvh);
+                    info[kInfoK + lane] = ps.k[0];
+                    info[kInfoV + lane] = ps.v_log2[0];
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(i_full + 8 * (j % kInfo));
+        };
+        // Tiles with keys that some row does not see.
+        auto edge = [&](int j) { return (j0 + j + 1) * kKeys > seen0; };
         if constexpr (BF16) {
-            cp_async_wait<0>();
-            if (!lost && steps > 0) {
+            // K: a gather of four pages brings one 16-byte column of each (B
+            // tokens of 8 head dims) to consecutive addresses of the tile's
+            // column; each warp takes half the columns.  V: a page at a time,
+            // swizzled as the product wants its rows of B tokens.  Few, large
+            // requests matter: one costs its warp about 60 cycles, and loads
+            // through registers would take the issue slots and the memory pipe
+            // that the softmax warps read TMEM with.
+            constexpr int CG = D / 8;  // columns of a K page
+            const bool first = warp == kSoftmaxWarps;
+            int landed[kStages] = {};
+            for (int j = 0; j < steps; ++j) {
+                const int st = j % kStages;
+                const int ids = next;
+                next = page_id(j + 1);
+                if (!wait(k_empty + 8 * st, j / kStages + 1)) break;
+                if (first) {
+                    page_info(j, ids);
+                    if (lane == 0) mbar_arrive_expect_tx(k_full + 8 * st, L::kTile);
+                    __syncwarp();
+                }
+                const uint32_t kdst = sbase + L::k + st * L::kTile;
+#pragma unroll
+                for (int g = 0; g < NPG / 4; ++g) {
+                    int page[4];  // (an illegal page's keys are masked: any page will do)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int id = __shfl_sync(kFull, ids, 4 * g + i);
+                        page[i] = (id < 0 ? 0 : id) * p.Hk + kvh;
+                    }
+                    if (lane < CG / 2) {
+                        const int c = lane + (first ? 0 : CG / 2);
+                        tma_gather4(kdst + c * (kKeys * 16) + g * (4 * B * 16), &maps.k, c * B * 8,
+                                    page[0], page[1], page[2], page[3], k_full + 8 * st);
+                    }
+                    __syncwarp();
+                }
+                if (first) {
+                    if (!wait(v_empty + 8 * st, j / kStages + 1)) break;
+                    const uint32_t bar = (edge(j) ? v_land : v_full) + 8 * st;
+                    if (lane == 0) mbar_arrive_expect_tx(bar, NPG * PAGE);
+                    __syncwarp();
+                    if (lane < NPG)  // (an illegal page is outside the map: zeros)
+                        tma_load_3d(sbase + L::v + st * L::kVTile + lane * PAGE, &maps.v, 0, 0,
+                                    ids >= 0 ? ids * p.Hk + kvh : p.v_pages, bar);
+                } else if (edge(j)) {
+                    // The second warp scrubs V where some row does not see every key.
+                    if (!wait(v_land + 8 * st, landed[st]++)) break;
+                    constexpr int PC = B / 8;  // 16-byte pieces of a row, a lane's always the same
+                    constexpr int kPieces = D * PC / 32;  // of a page, per lane
+                    constexpr int U = kPieces < 8 ? kPieces : 8;
+                    static_assert(kPieces % U == 0, "a page's pieces, no more");
+#pragma unroll 1
+                    for (int pg = 0; pg < NPG; ++pg) {
+                        const int key = (j0 + j) * kKeys + pg * B + lane % PC * 8;
+                        if ((j0 + j) * kKeys + (pg + 1) * B <= seen0) continue;
+                        const Late m = late_keys(key);
+                        const uint32_t page = sbase + L::v + st * L::kVTile + pg * PAGE;
+#pragma unroll 1
+                        for (int i0 = lane; i0 < D * PC; i0 += 32 * U) {
+                            uint4 w[U];
+                            uint32_t at[U];
+#pragma unroll
+                            for (int u = 0; u < U; ++u) {
+                                // The swizzle: bit 4 of the offset by bit 7 (rows
+                                // of 32 bytes), or bits 4, 5 by 7, 8 (of 64).
+                                const uint32_t off = (i0 + 32 * u) * 16;
+                                at[u] = page + (off ^ ((off >> 3) & (B == 16 ? 0x10u : 0x30u)));
+                                w[u] = lds128(at[u]);
+                            }
+#pragma unroll
+                            for (int u = 0; u < U; ++u) {
+                                if (odd_any(w[u], m)) {
+                                    scrub(w[u], m, key);
+                                    sts128(at[u], w[u]);
+                                }
+                            }
+                        }
+                    }
+                    fence_smem_to_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(v_full + 8 * st);
+                }
+            }
+            if (lost) {
+                // Copies in flight land before the CTA's memory is another's.
+                for (int i = 0; i < kStages; ++i)
+                    for (int ph = 0; ph < 2; ++ph) {
+                        (void)mbar_wait_bounded(k_full + 8 * i, ph, kDrainNs);
+                        (void)mbar_wait_bounded(v_full + 8 * i, ph, kDrainNs);
+                        (void)mbar_wait_bounded(v_land + 8 * i, ph, kDrainNs);
+                    }
+            }
+        } else {
+            // ---- 8-bit pages: warp 8 widens the K tiles, warp 9 the V tiles.  A
+            // page is 16-byte pieces, of K (column group, token), of V (head
+            // dim, tokens), taken by consecutive lanes; a lane's next piece of
+            // the page is a fixed step further at both ends.
+            const bool keys = warp == kSoftmaxWarps;
+            const uint32_t full = keys ? k_full : v_full, empty = keys ? k_empty : v_empty;
+            const uint8_t* cache = (keys ? p.kc : p.vc) + head_off + lane * 16;
+            constexpr int NQ = PAGE / 512;  // pieces of a page per lane
+            constexpr int VR = B / 16;      // pieces of a V row
+            static_assert(NQ * 512 == PAGE && 32 % B == 0, "");
+            // K: column group lane / B, token lane % B.  V: head dim lane / VR,
+            // part lane % VR.  A piece becomes two 16-byte columns.
+            const uint32_t column = keys ? kKeys * 16 : L::kVStep;
+            const uint32_t base =
+                keys ? sbase + L::k + 2 * (lane / B) * column + lane % B * 16
+                     : sbase + L::v + 2 * (lane % VR) * column + lane / VR * 16;
+            const uint32_t stage_bytes = keys ? L::kTile : L::kVTile;
+            const uint32_t page_step = keys ? B * 16 : B / 8 * L::kVStep;
+            const uint32_t piece_step = keys ? 2 * (32 / B) * column : 32 / VR * 16;
+            auto source = [&](int ids, int pg, bool& there) {
+                const int id = __shfl_sync(kFull, ids, pg);
+                there = id >= 0;
+                return cache + (there ? id : 0) * block_stride;
+            };
+            // Half a tile of codes is in registers while the other is in flight.
+            constexpr int HP = NPG / 2;
+            uint4 lo[HP][NQ], hi[HP][NQ];
+            auto fetch = [&](int ids, int pg0, uint4 (&w)[HP][NQ]) {
+#pragma unroll
+                for (int i = 0; i < HP; ++i) {
+                    bool there;
+                    const uint8_t* src = source(ids, pg0 + i, there);
+#pragma unroll
+                    for (int q = 0; q < NQ; ++q) {
+                        w[i][q] = make_uint4(0, 0, 0, 0);
+                        if (there) w[i][q] = __ldg(reinterpret_cast<const uint4*>(src + q * 512));
+                    }
+                }
+            };
+            auto put = [&](int j, int pg0, uint4 (&w)[HP][NQ]) {
+                if (!INT8 && !keys && edge(j)) {
+#pragma unroll
+                    for (int i = 0; i < HP; ++i) {
+                        const int key = (j0 + j) * kKeys + (pg0 + i) * B + lane % VR * 16;
+                        const Late m = late_keys(key);
+#pragma unroll
+                        for (int q = 0; q < NQ; ++q)
+                            if (odd_any(w[i][q], m)) scrub(w[i][q], m, key);
+                    }
+                }
+                const uint32_t dst = base + j % kStages * stage_bytes;
+#pragma unroll
+                for (int i = 0; i < HP; ++i)
+#pragma unroll
+                    for (int q = 0; q < NQ; ++q) {
+                        const uint32_t at = dst + (pg0 + i) * page_step + q * piece_step;
+                        put16(at, at + column, w[i][q]);
+                    }
+            };
+            int ids = next;
+            next = page_id(1);
+            fetch(ids, 0, lo);
+            for (int j = 0; j < steps; ++j) {
+                const int st = j % kStages;
+                fetch(ids, HP, hi);
+                if (!wait(empty + 8 * st, j / kStages + 1)) break;
+                if (keys) page_info(j, ids);
+                put(j, 0, lo);
+                ids = next;
+                next = page_id(j + 2);
+                fetch(ids, 0, lo);
+                put(j, HP, hi);
                 fence_smem_to_async();
-                mbar_arrive(v_full + 8 * ((steps - 1) % kStages));
+                mbar_arrive(full + 8 * st);
             }
         }
     } else if (warp == kMmaWarp) {
@@ -465,14 +515,20 @@ __global__ void __launch_bounds__(kCtaThreads, 1) pa_prefill_kernel(const Prefil
                                         kKeys * 16),
                            kQk, k > 0);
             };
-            auto values = [&](int t, int st, bool add) {
+            auto values = [&](int t, int st, int k0, int k1, bool add) {
 #pragma unroll
-                for (int k = 0; k < kKeys / 16; ++k)
-                    mma_ts(tmem + kTiles * kKeys + t * 128, tmem + t * kKeys + 8 * k,
-                           smem_operand(sbase + L::v + st * L::kTile + k * (2 * D * 16), D * 16),
-                           kPv, add || k > 0);
+                for (int k = k0; k < k1; ++k)
+                {
+                    const uint32_t v = sbase + L::v + st * L::kVTile;
+                    const uint64_t operand =
+                        !BF16     ? smem_operand(v + k * (2 * L::kVStep), L::kVStep)
+                        : B == 16 ? smem_operand_swizzled<32>(v + k * PAGE)
+                                  : smem_operand_swizzled<64>(v + k / 2 * PAGE + k % 2 * 32);
+                    mma_ts(tmem + kTiles * kKeys + t * 128, tmem + t * kKeys + 8 * k, operand, kPv,
+                           add || k > 0);
+                }
             };
-            if (steps > 0 && wait_one(k_full, 0)) {
+            if (steps > 0 && wait_one(q_full, 0) && wait_one(k_full, 0)) {
                 tmem_fence_after();
                 if (n0 > 0) {
                     scores(0, 0);
@@ -490,9 +546,12 @@ __global__ void __launch_bounds__(kCtaThreads, 1) pa_prefill_kernel(const Prefil
                 for (int t = 0; t < kTiles; ++t) {
                     const int nt = t ? n1 : n0;
                     if (j >= nt) continue;
+                    if (!wait_one(p_first + 8 * t, j)) break;
+                    tmem_fence_after();
+                    values(t, st, 0, kFirstKeys / 16, j > 0);
                     if (!wait_one(p_ready + 8 * t, j)) break;
                     tmem_fence_after();
-                    values(t, st, j > 0);
+                    values(t, st, kFirstKeys / 16, kKeys / 16, true);
                     if (j + 1 < nt) {
                         if (!wait_one(k_full + 8 * nx, (j + 1) / kStages)) break;
                         tmem_fence_after();
@@ -526,56 +585,121 @@ __global__ void __launch_bounds__(kCtaThreads, 1) pa_prefill_kernel(const Prefil
         // it does not make its warp mask (its results go nowhere).
         const int seen = row_ok ? T - n + qt + 1 : 0x7fffffff;
         float mul = p.scale_log2, out_mul = 1.f;
+        const uint32_t stage = sbase + L::q + t * L::kTile + warp % 4 * (32 * D * 2);
+        const int head = kvh * p.G + r % p.G;
+        const long long row = (static_cast<long long>(a) + qt) * p.Hq + head;
+        {
+            // The query row, as row r of the tile's operand (16 r of each
+            // 16-byte column).  f16 operands (8-bit caches) are scaled per row by
+            // a power of two, which puts the largest |q| in [2^14, 2^15).
+            // A warp reads whole rows, and turns them to a row per lane through
+            // its share of the tile (16-byte pieces rotated by the row).
+            constexpr int LR = D / 8, RI = 32 / LR;  // lanes per row, rows at a time
+            uint4 w[LR];
+#pragma unroll
+            for (int i = 0; i < LR; ++i) {
+                const long long from = __shfl_sync(kFull, row_ok ? row : -1ll, i * RI + lane / LR);
+                w[i] = make_uint4(0, 0, 0, 0);
+                if (from >= 0)
+                    w[i] = __ldg(reinterpret_cast<const uint4*>(p.q + from * D) + lane % LR);
+            }
+#pragma unroll
+            for (int i = 0; i < LR; ++i) {
+                const int to = i * RI + lane / LR;
+                sts128(stage + to * (D * 2) + ((lane ^ to) & (LR - 1)) * 16, w[i]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < LR; ++c)
+                w[c] = lds128(stage + lane * (D * 2) + ((c ^ lane) & (LR - 1)) * 16);
+            named_barrier(1 + t, kRows);  // the tile's four warps have their rows
+            float up = 1.f;
+            if constexpr (!BF16) {
+                float amax = 0.f;
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(x[k])), fabsf(bf16_hi(x[k]))));
+                }
+                int e = 0;  // amax in [2^(14 + e), 2^(15 + e))
+                if (amax > 0.f && amax < INFINITY)
+                    e = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14;
+                e = max(-110, min(113, e));
+                up = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                mul *= __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+                if constexpr (!BLOCK) {
+                    mul *= fabsf(__ldg(p.k_scale));
+                    out_mul = __ldg(p.v_scale);
+                }
+            }
+            // (Above 0, so that the -inf of a hidden key stays one.)
+            mul = fmaxf(mul, kTinyFactor);
+            const uint32_t flip = p.negate ? 0x80008000u : 0u;
+            const uint32_t dst = sbase + L::q + t * L::kTile + r * 16;
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+                uint32_t x[4] = {w[c].x ^ flip, w[c].y ^ flip, w[c].z ^ flip, w[c].w ^ flip};
+                if constexpr (!BF16) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        x[k] = pack_f16x2(bf16_lo(x[k]) * up, bf16_hi(x[k]) * up);
+                }
+                sts128(dst + c * (kRows * 16), make_uint4(x[0], x[1], x[2], x[3]));
+            }
+            fence_smem_to_async();
+            mbar_arrive(q_full);
+        }
         float m = -INFINITY, l = 0.f;
         for (int j = 0; j < nt && !lost; ++j) {
             if (!wait(s_ready + 8 * t, j)) break;
             if (!wait(i_full + 8 * (j % kInfo), j / kInfo)) break;
             tmem_fence_after();
-            if constexpr (!BF16) {
-                if (j == 0) {
-                    mul *= reinterpret_cast<const float*>(smem + L::q_mul)[t * kRows + r];
-                    if constexpr (!BLOCK) {
-                        mul *= fabsf(__ldg(p.k_scale));
-                        out_mul = __ldg(p.v_scale);
-                    }
-                }
-            }
             const float* info = reinterpret_cast<const float*>(smem + L::info) + (j % kInfo) * 32;
             const uint32_t legal = reinterpret_cast<const uint32_t*>(info)[0];
             const int left = seen - (j0 + j) * kKeys;  // keys of this tile that the row sees
-            const bool masked =
-                __any_sync(kFull, left < kKeys) || legal != (1u << NPG) - 1u;
-            // A column's score, -inf where the row does not see its key.
-            auto visible = [&](int c) {
-                return c < left && ((legal >> (c / B)) & 1u);
-            };
-            uint32_t x[32];
-            // ---- the tile's maximum (of x + log2 vs with block scales)
-            float mx = -INFINITY;
+            const bool masked = __any_sync(kFull, left < kKeys) || legal != (1u << NPG) - 1u;
+            // ---- the tile's scores, and their maximum (of x + log2 vs with
+            // block scales), the second half arriving behind the first
+            float x[kKeys], mx = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < kKeys; c += 32) {
-                tmem_ld32(s_at + c, x);
+            for (int c = 0; c < kKeys / 2; c += 32) tmem_ld32(s_at + c, x + c);
+#pragma unroll
+            for (int h = 0; h < kKeys; h += kKeys / 2) {
                 tmem_wait_ld();
+                if (h == 0) {
+#pragma unroll
+                    for (int c = kKeys / 2; c < kKeys; c += 32) tmem_ld32(s_at + c, x + c);
+                }
                 if (masked) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (!visible(c + i)) x[i] = 0xff800000u;
+                    for (int c = h; c < h + kKeys / 2; ++c)
+                        if (c >= left || !((legal >> (c / B)) & 1u)) x[c] = -INFINITY;
                 }
+                if constexpr (BLOCK) {
 #pragma unroll
-                for (int g = 0; g < 32; g += 16) {
-                    float y = __uint_as_float(x[g]);
+                    for (int pg = h / B; pg < (h + kKeys / 2) / B; ++pg) {
+                        float y = fmaxf(x[pg * B], x[pg * B + 1]);
 #pragma unroll
-                    for (int i = 1; i < 16; ++i) y = fmaxf(y, __uint_as_float(x[g + i]));
-                    const int pg = (c + g) / B;
-                    if constexpr (BLOCK) {
-                        // (-inf stays: a page's scale of 0 must not make it NaN)
-                        const float z = fmaf(y, mul * info[kInfoK + pg], info[kInfoV + pg]);
-                        y = y == -INFINITY ? y : z;
+                        for (int c = 2; c < B; c += 2)
+                            y = fmaxf(fmaxf(y, x[pg * B + c]), x[pg * B + c + 1]);
+                        const float f = fmaxf(mul * info[kInfoK + pg], kTinyFactor);
+                        mx = fmaxf(mx, fmaf(y, f, info[kInfoV + pg]));
                     }
-                    mx = fmaxf(mx, y);
+                } else {
+                    float y[4] = {x[h], x[h + 1], x[h + 2], x[h + 3]};
+#pragma unroll
+                    for (int c = h + 4; c + 8 <= h + kKeys / 2; c += 8)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            y[i] = fmaxf(fmaxf(y[i], x[c + 2 * i]), x[c + 2 * i + 1]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) y[i] = fmaxf(y[i], x[h + kKeys / 2 - 4 + i]);
+                    mx = fmaxf(mx, fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])));
                 }
             }
-            if constexpr (!BLOCK) mx = mx == -INFINITY ? mx : mx * mul;
+            if constexpr (!BLOCK) mx *= mul;
             // ---- O in the units of a new maximum, only when it grew by a lot
             const bool grow = mx > m + kLazyRescale || (m == -INFINITY && mx > -INFINITY);
             if (__any_sync(kFull, grow)) {
@@ -584,65 +708,60 @@ __global__ void __launch_bounds__(kCtaThreads, 1) pa_prefill_kernel(const Prefil
                 m = to;
                 l *= alpha;
                 if (j > 0) {
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < D; c += 32) {
-                        tmem_ld32(o_at + c, x);
+                        float o[32];
+                        tmem_ld32(o_at + c, o);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            x[i] = __float_as_uint(__uint_as_float(x[i]) * alpha);
-                        tmem_st32(o_at + c, x);
+                        for (int i = 0; i < 32; ++i) o[i] *= alpha;
+                        tmem_st32(o_at + c, o);
                     }
                 }
             }
             const float m_use = m == -INFINITY ? 0.f : m;
             // ---- weights back to TMEM over the scores; their sum
+            float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
             for (int c = 0; c < kKeys; c += 32) {
-                tmem_ld32(s_at + c, x);
-                tmem_wait_ld();
-                if (masked) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (!visible(c + i)) x[i] = 0xff800000u;
-                }
                 uint32_t w[16];
 #pragma unroll
                 for (int g = 0; g < 32; g += 16) {
                     const int pg = (c + g) / B;
-                    float f = mul, add = -m_use, back = 1.f;
+                    float f = mul, add = -m_use;
                     if constexpr (BLOCK) {
-                        f = mul * info[kInfoK + pg];
+                        f = fmaxf(mul * info[kInfoK + pg], kTinyFactor);
                         add = info[kInfoV + pg] - m_use;
-                        back = fast_exp2(-info[kInfoV + pg]);
                     }
-                    float s0 = 0.f, s1 = 0.f;
+                    const float2 f2 = make_float2(f, f), add2 = make_float2(add, add);
+                    float2 part = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int i = 0; i < 16; i += 2) {
-                        float y0 = fmaf(__uint_as_float(x[g + i]), f, add);
-                        float y1 = fmaf(__uint_as_float(x[g + i + 1]), f, add);
-                        if (masked) {  // a factor of 0 makes NaN of -inf
-                            if (x[g + i] == 0xff800000u) y0 = -INFINITY;
-                            if (x[g + i + 1] == 0xff800000u) y1 = -INFINITY;
-                        }
-                        const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
-                        s0 += p0;
-                        s1 += p1;
-                        w[(g + i) / 2] = BF16 ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
+                        const float2 y =
+                            __ffma2_rn(make_float2(x[c + g + i], x[c + g + i + 1]), f2, add2);
+                        const float2 e = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+                        part = __fadd2_rn(part, e);
+                        w[(g + i) / 2] = BF16 ? pack_bf16x2(e.x, e.y) : pack_f16x2(e.x, e.y);
                     }
-                    l = BLOCK ? fmaf(s0 + s1, back, l) : l + (s0 + s1);
+                    if constexpr (BLOCK) {
+                        const float back = fast_exp2(-info[kInfoV + pg]);
+                        sum = __ffma2_rn(part, make_float2(back, back), sum);
+                    } else {
+                        sum = __fadd2_rn(sum, part);
+                    }
                 }
                 tmem_st16(s_at + c / 2, w);
+                if (c + 32 == kFirstKeys || c + 32 == kKeys) {
+                    tmem_wait_st();
+                    tmem_fence_before();
+                    mbar_arrive((c + 32 == kKeys ? p_ready : p_first) + 8 * t);
+                }
             }
-            tmem_wait_st();
-            tmem_fence_before();
-            mbar_arrive(p_ready + 8 * t);
+            l += sum.x + sum.y;
         }
         // ---- the rows' results
         if (nt > 0) (void)wait(s_ready + 8 * t, nt);
         tmem_fence_after();
-        const int head = kvh * p.G + r % p.G;
-        const long long row = (static_cast<long long>(a) + qt) * p.Hq + head;
         const long long prow = row * p.P + part;
         const bool empty = nt == 0 || lost;
         if (p.P > 1 && row_ok) {
@@ -657,12 +776,9 @@ __global__ void __launch_bounds__(kCtaThreads, 1) pa_prefill_kernel(const Prefil
             for (int i = 0; i < 8; ++i) any_bad |= bad[i];
 #pragma unroll
             for (int c = 0; c < D; c += 32) {
-                uint32_t x[32];
-                tmem_ld32(o_at + c, x);
-                tmem_wait_ld();
                 float o[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(x[i]);
+                tmem_ld32(o_at + c, o);
+                tmem_wait_ld();
                 if (any_bad && row_ok) {
                     // Non-finite values of keys that not every row of the CTA
                     // sees were left out: they make the rows that do see them
@@ -693,21 +809,35 @@ __global__ void __launch_bounds__(kCtaThreads, 1) pa_prefill_kernel(const Prefil
                         }
                     }
                 }
-                if (!row_ok || lost) continue;
                 if (p.P > 1) {
+                    if (!row_ok || lost) continue;
                     float4* dst = reinterpret_cast<float4*>(p.ws_o + prow * D + c);
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         dst[i] = make_float4(o[4 * i] * inv, o[4 * i + 1] * inv,
                                              o[4 * i + 2] * inv, o[4 * i + 3] * inv);
                 } else {
-                    uint4* dst = reinterpret_cast<uint4*>(p.out + row * D + c);
+                    // Through the warp's rows of the (spent) Q tile, 16-byte
+                    // pieces rotated by the row, so that whole rows are stored.
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        dst[i] = make_uint4(pack_bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv),
-                                            pack_bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                            pack_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                                            pack_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+                        sts128(stage + lane * (D * 2) + (((c / 8 + i) ^ lane) & (D / 8 - 1)) * 16,
+                               make_uint4(pack_bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv),
+                                          pack_bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                          pack_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                                          pack_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv)));
+                }
+            }
+            if (p.P == 1 && !lost) {
+                __syncwarp();
+                constexpr int LR = D / 8, RI = 32 / LR;  // lanes per row, rows at a time
+#pragma unroll 4
+                for (int i = 0; i < 32; i += RI) {
+                    const int from = i + lane / LR;  // row of the warp
+                    const long long to = __shfl_sync(kFull, row_ok ? row : -1ll, from);
+                    if (to >= 0)
+                        *reinterpret_cast<uint4*>(p.out + to * D + lane % LR * 8) =
+                            lds128(stage + from * (D * 2) + ((lane ^ from) & (LR - 1)) * 16);
                 }
             }
         }
@@ -744,13 +874,54 @@ __global__ void __launch_bounds__(kThreads)
     });
 }
 
+// The maps of bf16 caches; false when the driver cannot make them.
+bool encode_maps(PageMaps* maps, const PrefillParams& p, int D, int B) {
+    using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static Encode encode = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
+                                             cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            encode = reinterpret_cast<Encode>(f);
+        (void)cudaGetLastError();
+    });
+    if (!encode) return false;
+    const auto u64 = [](long long x) { return static_cast<cuuint64_t>(x); };
+    const auto u32 = [](int x) { return static_cast<cuuint32_t>(x); };
+    const cuuint64_t v_dims[3] = {u64(B), u64(D), u64(p.v_pages)};
+    const cuuint64_t v_strides[2] = {u64(B * 2), u64(B * D * 2)};
+    const cuuint32_t v_box[3] = {u32(B), u32(D), 1};
+    const cuuint64_t k_dims[2] = {u64(B * D), u64(p.v_pages)};
+    const cuuint64_t k_strides[1] = {u64(B * D * 2)};
+    const cuuint32_t k_box[2] = {u32(B * 8), 1};
+    const cuuint32_t step[3] = {1, 1, 1};
+    return encode(&maps->v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint8_t*>(p.vc),
+                  v_dims, v_strides, v_box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  B == 16 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS &&
+           encode(&maps->k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint8_t*>(p.kc),
+                  k_dims, k_strides, k_box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, int B, int FMT>
 cudaError_t launch_prefill(const PrefillParams& p, unsigned grid, cudaStream_t st) {
     static std::atomic<int> done[kMaxDevices];
     auto kern = pa_prefill_kernel<D, B, FMT>;
     cudaError_t e = ensure_smem(kern, done);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, grid, kCtaThreads, Layout<D, FMT>::total, st, p);
+    PageMaps maps;
+    std::memset(&maps, 0, sizeof maps);
+    if (FMT == kFmtBf16 && !encode_maps(&maps, p, D, B)) return cudaErrorInvalidValue;
+    return launch_pdl(kern, grid, kCtaThreads, Layout<D, B, FMT == kFmtBf16>::total, st, p, maps);
 }
 
 template <int D, int B>
@@ -878,7 +1049,10 @@ extern "C" pa_status pa_prefill(void* out, const void* query, const void* key_ca
     if (static_cast<long long>(max_seq_len) >
         static_cast<long long>(max_blocks_per_seq) * block_size)
         return fail(PA_ERR_INVALID_ARG, "%s", "max_seq_len > max_blocks_per_seq * block_size");
-    if (num_blocks < 1) return fail(PA_ERR_INVALID_ARG, "%s", "num_blocks < 1");
+    if (num_blocks < 1 || num_blocks * num_kv_heads > 0x7ffffffeLL ||
+        num_blocks > 0x7ffffffeLL)
+        return fail(PA_ERR_INVALID_ARG, "%s",
+                    "num_blocks and num_blocks * num_kv_heads must be in [1, 2^31 - 1)");
     if (num_tokens == 0 || num_seqs == 0) return PA_OK;
     const struct {
         const void* p;
@@ -940,6 +1114,7 @@ extern "C" pa_status pa_prefill(void* out, const void* query, const void* key_ca
     p.units = static_cast<int>(pl.units);
     p.scale_log2 = static_cast<float>(std::fabs(static_cast<double>(scale)) * 1.4426950408889634);
     p.negate = scale < 0.f;
+    p.v_pages = static_cast<int>(num_blocks * num_kv_heads);
     const unsigned grid = static_cast<unsigned>(pl.units * num_kv_heads * pl.P);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
