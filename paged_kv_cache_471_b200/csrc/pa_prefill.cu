@@ -46,12 +46,10 @@ constexpr int kLoadWarps = 2;
 constexpr int kMmaWarp = kSoftmaxWarps + kLoadWarps;
 constexpr int kCtaThreads = (kMmaWarp + 1) * 32;
 constexpr uint32_t kTmemColumns = 512;  // S of both tiles, then O of both
-#ifndef PA_SPLIT
-#define PA_SPLIT 2
-#endif
 // The weights of a tile go to the product in two parts, the first of
-// kFirstKeys keys, so that it begins before the last weight is there.
-constexpr int kFirstKeys = 32 * PA_SPLIT;
+// kFirstKeys keys, so that it begins before the last weight is there (32, 64
+// and 96 keys measured within 1%).
+constexpr int kFirstKeys = 96;
 constexpr float kLazyRescale = 8.f;     // log2 of the largest weight
 constexpr int kMaxSplits = 32;          // partials per row (merge_slots)
 constexpr unsigned long long kWaitNs = 2000000000ull;
@@ -137,7 +135,8 @@ constexpr int kInfoK = 8, kInfoV = 16;
 constexpr float kTinyFactor = 1e-30f;  // of a logit: what is below counts as it
 
 template <int D, int B, int FMT>
-__global__ void __launch_bounds__(kCtaThreads, 1) pa_prefill_kernel(const PrefillParams p, const __grid_constant__ PageMaps maps) {
+__global__ void __launch_bounds__(kCtaThreads, 1)
+    pa_prefill_kernel(const PrefillParams p, const __grid_constant__ PageMaps maps) {
     using L = Layout<D, B, FMT == kFmtBf16>;
     constexpr bool BF16 = FMT == kFmtBf16;
     constexpr bool BLOCK = FMT == kFmtE4m3Block || FMT == kFmtInt8Block;
@@ -612,7 +611,10 @@ __global__ void __launch_bounds__(kCtaThreads, 1) pa_prefill_kernel(const Prefil
 #pragma unroll
             for (int c = 0; c < LR; ++c)
                 w[c] = lds128(stage + lane * (D * 2) + ((c ^ lane) & (LR - 1)) * 16);
-            named_barrier(1 + t, kRows);  // the tile's four warps have their rows
+            if (t == 0)  // the tile's four warps have their rows
+                named_barrier<1>(kRows);
+            else
+                named_barrier<2>(kRows);
             float up = 1.f;
             if constexpr (!BF16) {
                 float amax = 0.f;
@@ -661,45 +663,31 @@ __global__ void __launch_bounds__(kCtaThreads, 1) pa_prefill_kernel(const Prefil
             const int left = seen - (j0 + j) * kKeys;  // keys of this tile that the row sees
             const bool masked = __any_sync(kFull, left < kKeys) || legal != (1u << NPG) - 1u;
             // ---- the tile's scores, and their maximum (of x + log2 vs with
-            // block scales), the second half arriving behind the first
+            // block scales)
             float x[kKeys], mx = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < kKeys / 2; c += 32) tmem_ld32(s_at + c, x + c);
+            for (int c = 0; c < kKeys; c += 32) tmem_ld32(s_at + c, x + c);
+            tmem_wait_ld();
+            if (masked) {
 #pragma unroll
-            for (int h = 0; h < kKeys; h += kKeys / 2) {
-                tmem_wait_ld();
-                if (h == 0) {
-#pragma unroll
-                    for (int c = kKeys / 2; c < kKeys; c += 32) tmem_ld32(s_at + c, x + c);
-                }
-                if (masked) {
-#pragma unroll
-                    for (int c = h; c < h + kKeys / 2; ++c)
-                        if (c >= left || !((legal >> (c / B)) & 1u)) x[c] = -INFINITY;
-                }
-                if constexpr (BLOCK) {
-#pragma unroll
-                    for (int pg = h / B; pg < (h + kKeys / 2) / B; ++pg) {
-                        float y = fmaxf(x[pg * B], x[pg * B + 1]);
-#pragma unroll
-                        for (int c = 2; c < B; c += 2)
-                            y = fmaxf(fmaxf(y, x[pg * B + c]), x[pg * B + c + 1]);
-                        const float f = fmaxf(mul * info[kInfoK + pg], kTinyFactor);
-                        mx = fmaxf(mx, fmaf(y, f, info[kInfoV + pg]));
-                    }
-                } else {
-                    float y[4] = {x[h], x[h + 1], x[h + 2], x[h + 3]};
-#pragma unroll
-                    for (int c = h + 4; c + 8 <= h + kKeys / 2; c += 8)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            y[i] = fmaxf(fmaxf(y[i], x[c + 2 * i]), x[c + 2 * i + 1]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) y[i] = fmaxf(y[i], x[h + kKeys / 2 - 4 + i]);
-                    mx = fmaxf(mx, fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])));
-                }
+                for (int c = 0; c < kKeys; ++c)
+                    if (c >= left || !((legal >> (c / B)) & 1u)) x[c] = -INFINITY;
             }
-            if constexpr (!BLOCK) mx *= mul;
+            if constexpr (BLOCK) {
+#pragma unroll
+                for (int pg = 0; pg < NPG; ++pg) {
+                    float y = x[pg * B];
+#pragma unroll
+                    for (int c = 1; c < B; ++c) y = fmaxf(y, x[pg * B + c]);
+                    const float f = fmaxf(mul * info[kInfoK + pg], kTinyFactor);
+                    mx = fmaxf(mx, fmaf(y, f, info[kInfoV + pg]));
+                }
+            } else {
+                float y[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+                for (int c = 4; c < kKeys; ++c) y[c % 4] = fmaxf(y[c % 4], x[c]);
+                mx = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) * mul;
+            }
             // ---- O in the units of a new maximum, only when it grew by a lot
             const bool grow = mx > m + kLazyRescale || (m == -INFINITY && mx > -INFINITY);
             if (__any_sync(kFull, grow)) {

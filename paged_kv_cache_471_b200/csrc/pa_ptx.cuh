@@ -37,8 +37,9 @@ __device__ __forceinline__ void grid_dep_launch_dependents() {
 }
 
 // A barrier of `threads` threads of the CTA (whole warps), beside __syncthreads.
-__device__ __forceinline__ void named_barrier(int id, int threads) {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+template <int ID>
+__device__ __forceinline__ void named_barrier(int threads) {
+    asm volatile("bar.sync %0, %1;" ::"n"(ID), "r"(threads) : "memory");
 }
 
 // ---------------------------------------------------------------- mbarrier
