@@ -42,14 +42,16 @@ constexpr int kKeys = 128;        // keys of a tile
 constexpr int kStages = 2;        // K tiles, and V tiles, in shared memory
 constexpr int kInfo = 4;          // key tiles whose page info is kept
 constexpr int kSoftmaxWarps = 8;
-constexpr int kLoadWarps = 2;
-constexpr int kMmaWarp = kSoftmaxWarps + kLoadWarps;
-constexpr int kCtaThreads = (kMmaWarp + 1) * 32;
+// Loader warps (8-bit pages go through registers, and take one more), then the
+// warp that issues the products.  Either way a thread can have 168 registers.
+constexpr int load_warps(bool bf16) { return bf16 ? 2 : 3; }
+constexpr int cta_threads(bool bf16) { return (kSoftmaxWarps + load_warps(bf16) + 1) * 32; }
 constexpr uint32_t kTmemColumns = 512;  // S of both tiles, then O of both
 // The weights of a tile go to the product in two parts, the first of
 // kFirstKeys keys, so that it begins before the last weight is there (32, 64
 // and 96 keys measured within 1%).
 constexpr int kFirstKeys = 96;
+constexpr int kRawBytes = 8192;   // of codes in flight, per loader warp (8-bit pages)
 constexpr float kLazyRescale = 8.f;     // log2 of the largest weight
 constexpr int kMaxSplits = 32;          // partials per row (merge_slots)
 constexpr unsigned long long kWaitNs = 2000000000ull;
@@ -108,7 +110,11 @@ __device__ __forceinline__ int find_sequence(int S, int lane, First first, int x
 
 template <int D, int B, bool BF16>
 struct Layout {  // shared memory, in bytes
-    static constexpr int kTile = kRows * D * 2;  // a Q tile or a K tile
+    static constexpr int kTile = kKeys * D * 2;  // a K tile
+    // A Q tile: 8 head dims of every row, 16 bytes each.  The step between these
+    // columns is off the banks' period, so that lanes along a row store at once.
+    static constexpr int kQStep = kRows * 16 + 16;
+    static constexpr int kQTile = D / 8 * kQStep;
     // A V tile of bf16 pages: the pages as the TMA unit lays them down, rows of
     // B tokens with the 32- or 64-byte swizzle.  Of 8-bit pages: 8 keys of every
     // head dim, 16 bytes each, a step apart that is off the 128-byte period of
@@ -117,14 +123,17 @@ struct Layout {  // shared memory, in bytes
     static constexpr int kVStep = D * 16 + (B == 16 ? 64 : 32);
     static constexpr int kVTile = BF16 ? kTile : kKeys / 8 * kVStep;
     static constexpr int q = 0;
-    static constexpr int k = q + kTiles * kTile;
+    static constexpr int k = (q + kTiles * kQTile + 1023) / 1024 * 1024;
     static constexpr int v = k + kStages * kTile;
     static constexpr int info = v + kStages * kVTile;         // per key tile: 32 floats
-    static constexpr int bad = info + kInfo * 32 * 4;         // 8 words: see scrub
+    static constexpr int q_mul = info + kInfo * 32 * 4;       // per row: float (8-bit pages)
+    static constexpr int bad = q_mul + kTiles * kRows * 4;    // 8 words: see scrub
     static constexpr int bars = bad + 32;
     static constexpr int n_bars = 5 * kStages + 3 * kTiles + kInfo + 2;
     static constexpr int tmem_slot = bars + 8 * n_bars;
-    static constexpr int total = tmem_slot + 16;
+    // 8-bit pages as they come from the cache, kRawBytes for each loader warp.
+    static constexpr int raw = (tmem_slot + 16 + 127) / 128 * 128;
+    static constexpr int total = BF16 ? raw : raw + load_warps(BF16) * kRawBytes;
 };
 
 // Page info of a key tile: word 0, a bit per page with a legal block id; from
@@ -135,7 +144,7 @@ constexpr int kInfoK = 8, kInfoV = 16;
 constexpr float kTinyFactor = 1e-30f;  // of a logit: what is below counts as it
 
 template <int D, int B, int FMT>
-__global__ void __launch_bounds__(kCtaThreads, 1)
+__global__ void __launch_bounds__(cta_threads(FMT == kFmtBf16), 1)
     pa_prefill_kernel(const PrefillParams p, const __grid_constant__ PageMaps maps) {
     using L = Layout<D, B, FMT == kFmtBf16>;
     constexpr bool BF16 = FMT == kFmtBf16;
@@ -144,6 +153,7 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
     constexpr int ELEM = BF16 ? 2 : 1;
     constexpr int PAGE = D * B * ELEM;
     constexpr int NPG = kKeys / B;  // pages of a key tile
+    constexpr int kLoadWarps = load_warps(BF16), kMmaWarp = kSoftmaxWarps + kLoadWarps;
     extern __shared__ __align__(1024) uint8_t prefill_smem[];
     uint8_t* const smem = prefill_smem;
     grid_dep_wait();
@@ -201,8 +211,8 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
     uint32_t* bad = reinterpret_cast<uint32_t*>(smem + L::bad);
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(k_full + 8 * i, BF16 ? 1 : 32);
-            mbar_init(v_full + 8 * i, BF16 ? 1 : 32);
+            mbar_init(k_full + 8 * i, BF16 ? 1 : 32 * kLoadWarps);
+            mbar_init(v_full + 8 * i, BF16 ? 2 : 32 * kLoadWarps);
             mbar_init(v_land + 8 * i, 1);
             mbar_init(k_empty + 8 * i, 1);
             mbar_init(v_empty + 8 * i, 1);
@@ -249,7 +259,6 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
             return -1;
         };
         int next = page_id(0);
-
         auto widen = [&](uint32_t w, uint32_t& lo, uint32_t& hi) {
             lo = INT8 ? int8_lo_pair(w) : e4m3_lo_pair(w);
             hi = INT8 ? int8_hi_pair(w) : e4m3_hi_pair(w);
@@ -310,7 +319,15 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
             }
             w = make_uint4(x[0], x[1], x[2], x[3]);
         };
-        auto page_info = [&](int j, int ids) {
+        auto scales_of = [&](int ids) {
+            PageScales ps = {};
+            if constexpr (BLOCK) {
+                if (lane < NPG)
+                    ps = load_page_scales(p.k_scale, p.v_scale, ids, -1, p.num_blocks, p.Hk, kvh);
+            }
+            return ps;
+        };
+        auto page_info = [&](int j, int ids, [[maybe_unused]] const PageScales& ps) {
             // (kInfo tiles deep: the slot's last user is done once K of tile
             // j - 2 has been released.)
             float* info = reinterpret_cast<float*>(smem + L::info) + (j % kInfo) * 32;
@@ -318,8 +335,6 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
             if (lane == 0) reinterpret_cast<uint32_t*>(info)[0] = legal;
             if constexpr (BLOCK) {
                 if (lane < NPG) {
-                    const PageScales ps = load_page_scales(p.k_scale, p.v_scale, ids, -1,
-                                                           p.num_blocks, p.Hk, kvh);
                     info[kInfoK + lane] = ps.k[0];
                     info[kInfoV + lane] = ps.v_log2[0];
                 }
@@ -346,7 +361,7 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
                 next = page_id(j + 1);
                 if (!wait(k_empty + 8 * st, j / kStages + 1)) break;
                 if (first) {
-                    page_info(j, ids);
+                    page_info(j, ids, PageScales{});
                     if (lane == 0) mbar_arrive_expect_tx(k_full + 8 * st, L::kTile);
                     __syncwarp();
                 }
@@ -366,25 +381,30 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
                     }
                     __syncwarp();
                 }
+                if (!wait(v_empty + 8 * st, j / kStages + 1)) break;
+                const bool late = edge(j);
                 if (first) {
-                    if (!wait(v_empty + 8 * st, j / kStages + 1)) break;
-                    const uint32_t bar = (edge(j) ? v_land : v_full) + 8 * st;
+                    const uint32_t bar = (late ? v_land : v_full) + 8 * st;
                     if (lane == 0) mbar_arrive_expect_tx(bar, NPG * PAGE);
                     __syncwarp();
                     if (lane < NPG)  // (an illegal page is outside the map: zeros)
                         tma_load_3d(sbase + L::v + st * L::kVTile + lane * PAGE, &maps.v, 0, 0,
                                     ids >= 0 ? ids * p.Hk + kvh : p.v_pages, bar);
-                } else if (edge(j)) {
-                    // The second warp scrubs V where some row does not see every key.
+                } else if (!late && lane == 0) {
+                    mbar_arrive(v_full + 8 * st);
+                }
+                if (late) {
+                    // Each warp scrubs half the pages that some row does not see.
                     if (!wait(v_land + 8 * st, landed[st]++)) break;
                     constexpr int PC = B / 8;  // 16-byte pieces of a row, a lane's always the same
                     constexpr int kPieces = D * PC / 32;  // of a page, per lane
                     constexpr int U = kPieces < 8 ? kPieces : 8;
                     static_assert(kPieces % U == 0, "a page's pieces, no more");
 #pragma unroll 1
-                    for (int pg = 0; pg < NPG; ++pg) {
+                    for (int pg = first ? 0 : 1; pg < NPG; pg += 2) {
                         const int key = (j0 + j) * kKeys + pg * B + lane % PC * 8;
-                        if ((j0 + j) * kKeys + (pg + 1) * B <= seen0) continue;
+                        const int page_key = (j0 + j) * kKeys + pg * B;
+                        if (page_key + B <= seen0 || page_key >= seen_end) continue;
                         const Late m = late_keys(key);
                         const uint32_t page = sbase + L::v + st * L::kVTile + pg * PAGE;
 #pragma unroll 1
@@ -423,81 +443,86 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
                     }
             }
         } else {
-            // ---- 8-bit pages: warp 8 widens the K tiles, warp 9 the V tiles.  A
-            // page is 16-byte pieces, of K (column group, token), of V (head
-            // dim, tokens), taken by consecutive lanes; a lane's next piece of
-            // the page is a fixed step further at both ends.
-            const bool keys = warp == kSoftmaxWarps;
-            const uint32_t full = keys ? k_full : v_full, empty = keys ? k_empty : v_empty;
-            const uint8_t* cache = (keys ? p.kc : p.vc) + head_off + lane * 16;
+            // ---- 8-bit pages.  Those of all tiles, K's and V's of each tile in
+            // turn, are dealt to the loader warps one by one.  A page is 16-byte
+            // pieces, of K (column group, token), of V (head dim, tokens), taken by
+            // consecutive lanes; a lane's next piece of the page is a fixed step
+            // further at both ends.  Pages go through a ring of slots: asynchronous
+            // copies bring some while the one before is widened, and a lane reads
+            // what it copied itself.  The loop is kept short: unrolled over a tile
+            // it missed the instruction cache, and a tile took 2.5 times as long.
             constexpr int NQ = PAGE / 512;  // pieces of a page per lane
             constexpr int VR = B / 16;      // pieces of a V row
+            constexpr int kSlots = kRawBytes / PAGE < NPG / 2 ? kRawBytes / PAGE : NPG / 2;
             static_assert(NQ * 512 == PAGE && 32 % B == 0, "");
-            // K: column group lane / B, token lane % B.  V: head dim lane / VR,
-            // part lane % VR.  A piece becomes two 16-byte columns.
-            const uint32_t column = keys ? kKeys * 16 : L::kVStep;
-            const uint32_t base =
-                keys ? sbase + L::k + 2 * (lane / B) * column + lane % B * 16
-                     : sbase + L::v + 2 * (lane % VR) * column + lane / VR * 16;
-            const uint32_t stage_bytes = keys ? L::kTile : L::kVTile;
-            const uint32_t page_step = keys ? B * 16 : B / 8 * L::kVStep;
-            const uint32_t piece_step = keys ? 2 * (32 / B) * column : 32 / VR * 16;
-            auto source = [&](int ids, int pg, bool& there) {
-                const int id = __shfl_sync(kFull, ids, pg);
-                there = id >= 0;
-                return cache + (there ? id : 0) * block_stride;
-            };
-            // Half a tile of codes is in registers while the other is in flight.
-            constexpr int HP = NPG / 2;
-            uint4 lo[HP][NQ], hi[HP][NQ];
-            auto fetch = [&](int ids, int pg0, uint4 (&w)[HP][NQ]) {
+            static_assert(kSlots * kLoadWarps < 2 * NPG, "copies run ahead into the next tile");
+            const int me = warp - kSoftmaxWarps;
+            const uint32_t ring = sbase + L::raw + me * kRawBytes + lane * 16;
+            // Page i of a tile (K's, then V's) to a slot; ids are the tile's.
+            auto copy = [&](int ids, int i, uint32_t slot) {
+                const int id = __shfl_sync(kFull, ids, i % NPG);
+                const uint8_t* src = (i < NPG ? p.kc : p.vc) + (id < 0 ? 0 : id) * block_stride +
+                                     head_off + lane * 16;
 #pragma unroll
-                for (int i = 0; i < HP; ++i) {
-                    bool there;
-                    const uint8_t* src = source(ids, pg0 + i, there);
-#pragma unroll
-                    for (int q = 0; q < NQ; ++q) {
-                        w[i][q] = make_uint4(0, 0, 0, 0);
-                        if (there) w[i][q] = __ldg(reinterpret_cast<const uint4*>(src + q * 512));
-                    }
-                }
-            };
-            auto put = [&](int j, int pg0, uint4 (&w)[HP][NQ]) {
-                if (!INT8 && !keys && edge(j)) {
-#pragma unroll
-                    for (int i = 0; i < HP; ++i) {
-                        const int key = (j0 + j) * kKeys + (pg0 + i) * B + lane % VR * 16;
-                        const Late m = late_keys(key);
-#pragma unroll
-                        for (int q = 0; q < NQ; ++q)
-                            if (odd_any(w[i][q], m)) scrub(w[i][q], m, key);
-                    }
-                }
-                const uint32_t dst = base + j % kStages * stage_bytes;
-#pragma unroll
-                for (int i = 0; i < HP; ++i)
-#pragma unroll
-                    for (int q = 0; q < NQ; ++q) {
-                        const uint32_t at = dst + (pg0 + i) * page_step + q * piece_step;
-                        put16(at, at + column, w[i][q]);
-                    }
+                for (int q = 0; q < NQ; ++q)
+                    cp_async16(slot + q * 512, src + q * 512, id < 0 ? 0u : 16u);
+                cp_async_commit();
             };
             int ids = next;
+            PageScales scales = scales_of(ids);
             next = page_id(1);
-            fetch(ids, 0, lo);
-            for (int j = 0; j < steps; ++j) {
+            for (int i = 0; i < kSlots; ++i) copy(ids, me + i * kLoadWarps, ring + i * PAGE);
+            int slot = 0, i = me;  // the next page of this warp, within tile j
+            for (int j = 0; j < steps && !lost; ++j) {
                 const int st = j % kStages;
-                fetch(ids, HP, hi);
-                if (!wait(empty + 8 * st, j / kStages + 1)) break;
-                if (keys) page_info(j, ids);
-                put(j, 0, lo);
+                const PageScales now = scales;
+                scales = scales_of(next);
+                for (int v = 0; v < 2; ++v) {  // K's pages, then V's
+                    if (!wait((v ? v_empty : k_empty) + 8 * st, j / kStages + 1)) break;
+                    if (!v && me == 0) page_info(j, ids, now);
+                    // K: column group lane / B, token lane % B.  V: head dim lane /
+                    // VR, part lane % VR.  A piece becomes two 16-byte columns.
+                    const uint32_t column = v ? L::kVStep : kKeys * 16;
+                    const uint32_t dst =
+                        v ? sbase + L::v + st * L::kVTile + 2 * (lane % VR) * column + lane / VR * 16
+                          : sbase + L::k + st * L::kTile + 2 * (lane / B) * column + lane % B * 16;
+                    const uint32_t page_step = v ? B / 8 * L::kVStep : B * 16;
+                    const uint32_t piece_step = v ? 32 / VR * 16 : 2 * (32 / B) * column;
+                    const bool late = !INT8 && v && edge(j);
+#pragma unroll 1
+                    for (; i < (v + 1) * NPG; i += kLoadWarps) {
+                        cp_async_wait<kSlots - 1>();
+                        const uint32_t raw = ring + slot * PAGE;
+                        const int pg = i % NPG;
+                        uint4 w[NQ];
+#pragma unroll
+                        for (int q = 0; q < NQ; ++q) w[q] = lds128(raw + q * 512);
+                        if (late) {
+                            const int key = (j0 + j) * kKeys + pg * B + lane % VR * 16;
+                            const Late m = late_keys(key);
+#pragma unroll
+                            for (int q = 0; q < NQ; ++q)
+                                if (odd_any(w[q], m)) scrub(w[q], m, key);
+                        }
+#pragma unroll
+                        for (int q = 0; q < NQ; ++q) {
+                            const uint32_t at = dst + pg * page_step + q * piece_step;
+                            put16(at, at + column, w[q]);
+                        }
+                        // The slot's next page: of this tile, or of the next one
+                        // (none behind the last tile: zeros).
+                        const int ahead = i + kSlots * kLoadWarps;
+                        copy(ahead < 2 * NPG ? ids : next, ahead % (2 * NPG), raw);
+                        slot = slot + 1 == kSlots ? 0 : slot + 1;
+                    }
+                    fence_smem_to_async();
+                    mbar_arrive((v ? v_full : k_full) + 8 * st);
+                }
+                i -= 2 * NPG;
                 ids = next;
                 next = page_id(j + 2);
-                fetch(ids, 0, lo);
-                put(j, HP, hi);
-                fence_smem_to_async();
-                mbar_arrive(full + 8 * st);
             }
+            cp_async_wait<0>();
         }
     } else if (warp == kMmaWarp) {
         // ================================================ products
@@ -508,8 +533,8 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
                     mma_ss(tmem + t * kKeys,
-                           smem_operand(sbase + L::q + t * L::kTile + k * (2 * kRows * 16),
-                                        kRows * 16),
+                           smem_operand(sbase + L::q + t * L::kQTile + k * (2 * L::kQStep),
+                                        L::kQStep),
                            smem_operand(sbase + L::k + st * L::kTile + k * (2 * kKeys * 16),
                                         kKeys * 16),
                            kQk, k > 0);
@@ -584,53 +609,61 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
         // it does not make its warp mask (its results go nowhere).
         const int seen = row_ok ? T - n + qt + 1 : 0x7fffffff;
         float mul = p.scale_log2, out_mul = 1.f;
-        const uint32_t stage = sbase + L::q + t * L::kTile + warp % 4 * (32 * D * 2);
+        const uint32_t stage = sbase + L::q + t * L::kQTile + warp % 4 * (32 * D * 2);
         const int head = kvh * p.G + r % p.G;
         const long long row = (static_cast<long long>(a) + qt) * p.Hq + head;
         {
-            // The query row, as row r of the tile's operand (16 r of each
-            // 16-byte column).  f16 operands (8-bit caches) are scaled per row by
-            // a power of two, which puts the largest |q| in [2^14, 2^15).
-            // A warp reads whole rows, and turns them to a row per lane through
-            // its share of the tile (16-byte pieces rotated by the row).
+            // The warp's 32 query rows, 16 bytes a lane, into the tile's operand.
+            // f16 operands (8-bit caches) are scaled per row by a power of two,
+            // which puts the largest |q| in [2^14, 2^15).
             constexpr int LR = D / 8, RI = 32 / LR;  // lanes per row, rows at a time
-            uint4 w[LR];
+            const uint32_t flip = p.negate ? 0x80008000u : 0u;
+            float* muls = reinterpret_cast<float*>(smem + L::q_mul) + t * kRows + warp % 4 * 32;
+            constexpr int QB = 8;  // loads in flight
+#pragma unroll 1
+            for (int i0 = 0; i0 < LR; i0 += QB) {
+                uint4 w[QB];
 #pragma unroll
-            for (int i = 0; i < LR; ++i) {
-                const long long from = __shfl_sync(kFull, row_ok ? row : -1ll, i * RI + lane / LR);
-                w[i] = make_uint4(0, 0, 0, 0);
-                if (from >= 0)
-                    w[i] = __ldg(reinterpret_cast<const uint4*>(p.q + from * D) + lane % LR);
-            }
-#pragma unroll
-            for (int i = 0; i < LR; ++i) {
-                const int to = i * RI + lane / LR;
-                sts128(stage + to * (D * 2) + ((lane ^ to) & (LR - 1)) * 16, w[i]);
-            }
-            __syncwarp();
-#pragma unroll
-            for (int c = 0; c < LR; ++c)
-                w[c] = lds128(stage + lane * (D * 2) + ((c ^ lane) & (LR - 1)) * 16);
-            if (t == 0)  // the tile's four warps have their rows
-                named_barrier<1>(kRows);
-            else
-                named_barrier<2>(kRows);
-            float up = 1.f;
-            if constexpr (!BF16) {
-                float amax = 0.f;
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c) {
-                    const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(x[k])), fabsf(bf16_hi(x[k]))));
+                for (int u = 0; u < QB; ++u) {
+                    const long long from =
+                        __shfl_sync(kFull, row_ok ? row : -1ll, (i0 + u) * RI + lane / LR);
+                    w[u] = make_uint4(0, 0, 0, 0);
+                    if (from >= 0)
+                        w[u] = __ldg(reinterpret_cast<const uint4*>(p.q + from * D) + lane % LR);
                 }
-                int e = 0;  // amax in [2^(14 + e), 2^(15 + e))
-                if (amax > 0.f && amax < INFINITY)
-                    e = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14;
-                e = max(-110, min(113, e));
-                up = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-                mul *= __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+#pragma unroll
+                for (int u = 0; u < QB; ++u) {
+                    const int of = (i0 + u) * RI + lane / LR;  // row of the warp
+                    uint32_t x[4] = {w[u].x ^ flip, w[u].y ^ flip, w[u].z ^ flip, w[u].w ^ flip};
+                    if constexpr (!BF16) {
+                        float amax = 0.f;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(x[k])), fabsf(bf16_hi(x[k]))));
+#pragma unroll
+                        for (int o = LR / 2; o > 0; o >>= 1)
+                            amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
+                        int e = 0;  // amax in [2^(14 + e), 2^(15 + e))
+                        if (amax > 0.f && amax < INFINITY)
+                            e = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14;
+                        e = max(-110, min(113, e));
+                        const float up = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                        if (lane % LR == 0)
+                            muls[of] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            x[k] = pack_f16x2(bf16_lo(x[k]) * up, bf16_hi(x[k]) * up);
+                    }
+                    sts128(sbase + L::q + t * L::kQTile + lane % LR * L::kQStep +
+                               (warp % 4 * 32 + of) * 16,
+                           make_uint4(x[0], x[1], x[2], x[3]));
+                }
+            }
+            fence_smem_to_async();
+            mbar_arrive(q_full);
+            if constexpr (!BF16) {
+                __syncwarp();
+                mul *= muls[lane];
                 if constexpr (!BLOCK) {
                     mul *= fabsf(__ldg(p.k_scale));
                     out_mul = __ldg(p.v_scale);
@@ -638,26 +671,20 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
             }
             // (Above 0, so that the -inf of a hidden key stays one.)
             mul = fmaxf(mul, kTinyFactor);
-            const uint32_t flip = p.negate ? 0x80008000u : 0u;
-            const uint32_t dst = sbase + L::q + t * L::kTile + r * 16;
-#pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-                uint32_t x[4] = {w[c].x ^ flip, w[c].y ^ flip, w[c].z ^ flip, w[c].w ^ flip};
-                if constexpr (!BF16) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        x[k] = pack_f16x2(bf16_lo(x[k]) * up, bf16_hi(x[k]) * up);
-                }
-                sts128(dst + c * (kRows * 16), make_uint4(x[0], x[1], x[2], x[3]));
-            }
-            fence_smem_to_async();
-            mbar_arrive(q_full);
         }
+        // A warp without a row of a query token has nothing to weigh: whatever its
+        // rows' products are, they go nowhere.
+        const bool idle = !__any_sync(kFull, row_ok);
         float m = -INFINITY, l = 0.f;
         for (int j = 0; j < nt && !lost; ++j) {
             if (!wait(s_ready + 8 * t, j)) break;
             if (!wait(i_full + 8 * (j % kInfo), j / kInfo)) break;
             tmem_fence_after();
+            if (idle) {
+                mbar_arrive(p_first + 8 * t);
+                mbar_arrive(p_ready + 8 * t);
+                continue;
+            }
             const float* info = reinterpret_cast<const float*>(smem + L::info) + (j % kInfo) * 32;
             const uint32_t legal = reinterpret_cast<const uint32_t*>(info)[0];
             const int left = seen - (j0 + j) * kKeys;  // keys of this tile that the row sees
@@ -758,11 +785,11 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
             p.ws_l[prow] = empty ? 0.f : l != l ? 1.f : l;
         }
         const float inv = l > 0.f || l != l ? out_mul / l : 0.f;
-        if (nt > 0) {
+        if (nt > 0 && !idle) {
             uint32_t any_bad = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) any_bad |= bad[i];
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 float o[32];
                 tmem_ld32(o_at + c, o);
@@ -819,13 +846,20 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
             if (p.P == 1 && !lost) {
                 __syncwarp();
                 constexpr int LR = D / 8, RI = 32 / LR;  // lanes per row, rows at a time
-#pragma unroll 4
-                for (int i = 0; i < 32; i += RI) {
-                    const int from = i + lane / LR;  // row of the warp
-                    const long long to = __shfl_sync(kFull, row_ok ? row : -1ll, from);
-                    if (to >= 0)
-                        *reinterpret_cast<uint4*>(p.out + to * D + lane % LR * 8) =
-                            lds128(stage + from * (D * 2) + ((lane ^ from) & (LR - 1)) * 16);
+#pragma unroll 1
+                for (int i0 = 0; i0 < LR; i0 += 8) {
+                    uint4 w[8];
+                    long long to[8];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        const int from = (i0 + u) * RI + lane / LR;  // row of the warp
+                        to[u] = __shfl_sync(kFull, row_ok ? row : -1ll, from);
+                        w[u] = lds128(stage + from * (D * 2) + ((lane ^ from) & (LR - 1)) * 16);
+                    }
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        if (to[u] >= 0)
+                            *reinterpret_cast<uint4*>(p.out + to[u] * D + lane % LR * 8) = w[u];
                 }
             }
         }
@@ -903,13 +937,14 @@ bool encode_maps(PageMaps* maps, const PrefillParams& p, int D, int B) {
 template <int D, int B, int FMT>
 cudaError_t launch_prefill(const PrefillParams& p, unsigned grid, cudaStream_t st) {
     static std::atomic<int> done[kMaxDevices];
+    constexpr bool kBf16 = FMT == kFmtBf16;
     auto kern = pa_prefill_kernel<D, B, FMT>;
     cudaError_t e = ensure_smem(kern, done);
     if (e != cudaSuccess) return e;
     PageMaps maps;
     std::memset(&maps, 0, sizeof maps);
-    if (FMT == kFmtBf16 && !encode_maps(&maps, p, D, B)) return cudaErrorInvalidValue;
-    return launch_pdl(kern, grid, kCtaThreads, Layout<D, B, FMT == kFmtBf16>::total, st, p, maps);
+    if (kBf16 && !encode_maps(&maps, p, D, B)) return cudaErrorInvalidValue;
+    return launch_pdl(kern, grid, cta_threads(kBf16), Layout<D, B, kBf16>::total, st, p, maps);
 }
 
 template <int D, int B>
