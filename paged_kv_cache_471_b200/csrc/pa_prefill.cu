@@ -141,7 +141,7 @@ struct Layout {  // shared memory, in bytes
 // formats; 8 pages at most).
 constexpr int kInfoK = 8, kInfoV = 16;
 
-constexpr float kTinyFactor = 1e-30f;  // of a logit: what is below counts as it
+constexpr float kTinyFactor = 1.17549435e-38f;  // of a logit: what is below counts as it
 
 template <int D, int B, int FMT>
 __global__ void __launch_bounds__(cta_threads(FMT == kFmtBf16), 1)
@@ -617,7 +617,10 @@ __global__ void __launch_bounds__(cta_threads(FMT == kFmtBf16), 1)
             // f16 operands (8-bit caches) are scaled per row by a power of two,
             // which puts the largest |q| in [2^14, 2^15).
             constexpr int LR = D / 8, RI = 32 / LR;  // lanes per row, rows at a time
-            const uint32_t flip = p.negate ? 0x80008000u : 0u;
+            // (Factors of a logit stay above 0; a sign goes to the query.)
+            bool negate = p.negate != 0;
+            if constexpr (FMT == kFmtE4m3) negate ^= __ldg(p.k_scale) < 0.f;
+            const uint32_t flip = negate ? 0x80008000u : 0u;
             float* muls = reinterpret_cast<float*>(smem + L::q_mul) + t * kRows + warp % 4 * 32;
             constexpr int QB = 8;  // loads in flight
 #pragma unroll 1

@@ -125,6 +125,27 @@ def test_scales_of_any_sign(scale):
         check(out, cache, q, ends([150]), scale)
 
 
+def test_scales_of_any_sign_per_tensor():
+    """Per-tensor scales below 0 work as they do in decode."""
+    cache = Cache("fp8_e4m3", [200], 1, 64, 16, seed=6)
+    cache.ks, cache.vs = -cache.ks, -cache.vs
+    q = queries(150, 2, 64)
+    out = prefill(cache, q, ends([150]), 0.2)
+    check(out, cache, q, ends([150]), 0.2)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "int8_block"])
+def test_rows_before_the_first_sequence(kv):
+    """Rows below query_start[0] belong to nobody, with and without a split."""
+    new = [3, 0, 300]
+    cache = Cache(kv, [5, 9, 400], 2, 64, 16, seed=15)
+    q = queries(sum(new) + 37, 4, 64)
+    for pages in (0, 8):
+        out = prefill(cache, q, ends(new) + 37, 0.125, partition_pages=pages)
+        assert torch.isnan(out[:37].float()).all()
+        check(out[37:], cache, q[37:], ends(new), 0.125)
+
+
 def test_queries_beyond_f16():
     """8-bit caches meet the queries in f16: rows are scaled by a power of two."""
     cache = Cache("fp8_e4m3_block", [150], 1, 128, 16, seed=7)
@@ -262,5 +283,7 @@ def test_binding_refusals():
             64, dtype=torch.uint8, device=DEV))
     with pytest.raises(TypeError):
         prefill(cache, q.float(), ends([7, 3]), 0.1)
+    with pytest.raises(ValueError):
+        prefill(cache, q, torch.tensor([[0, 7, 10]], dtype=torch.int32), 0.1)
     out = prefill(cache, q[:0], ends([0, 0]), 0.1)
     assert out.numel() == 0
