@@ -319,6 +319,10 @@ __device__ __forceinline__ void append_keys(const AppendParams& p, const Run& r,
         const uint16_t* src = p.k + static_cast<long long>(r.row0 + t) * p.k_stride + h * D;
         wa = __ldg(reinterpret_cast<const uint4*>(src + 8 * cp.a));
         wb = __ldg(reinterpret_cast<const uint4*>(src + 8 * cp.b));
+        if (t + TPI < r.m) {
+            prefetch_l1(src + TPI * p.k_stride + 8 * cp.a);
+            prefetch_l1(src + TPI * p.k_stride + 8 * cp.b);
+        }
         Turn turn;
         turn.load<INTERLEAVED>(p, cp, position_of(p, r.row0 + t, r.index0 + t));
         x.turned<INTERLEAVED>(wa, wb, cp, turn);
@@ -394,10 +398,10 @@ __device__ __forceinline__ void append_keys(const AppendParams& p, const Run& r,
 
 // ---------------------------------------------------------------------- values
 // A V page holds a row of B tokens per head dim: lane l owns dims DV l ..
-// DV l + DV - 1 of every token (DV = D / 32).  Where the run fills 16 slots the
-// transposition happens in the lane's registers and each of its rows leaves as
-// one piece (32 bytes of bf16, 16 of codes); at the run's ends, and for single
-// tokens, elements are stored one by one.
+// DV l + DV - 1 of every token (DV = D / 32), and the transposition happens in
+// its registers.  Where the run fills 16 slots each of the lane's rows leaves as
+// one piece (32 bytes of bf16, 16 of codes), else as words of the slots that it
+// fills; at its ends, and for single tokens, elements are stored one by one.
 template <int D, int B, int FMT>
 __device__ __forceinline__ void append_values(const AppendParams& p, const Run& r, int h,
                                               long long pb, int lane) {
@@ -466,46 +470,63 @@ __device__ __forceinline__ void append_values(const AppendParams& p, const Run& 
         scale = __ldg(p.v_scale);
     }
     const int end = r.off + r.m;
+    constexpr int kPerWord = 4 / ELEM;  // slots of a 32-bit word of a row
     auto store = [&](const auto& div) {
 #pragma unroll 1
         for (int t0 = 0; t0 < B; t0 += kStep) {  // slots t0 .. t0 + 15
-            uint8_t* out = rows + t0 * ELEM;
-            if (r.off > t0 || end < t0 + kStep) {
-#pragma unroll 1
-                for (int t = max(t0, r.off); t < min(t0 + kStep, end); ++t) {
-                    uint32_t w[NW];
-                    load(t - r.off, w);
+            const int lo = max(t0, r.off), hi = min(t0 + kStep, end);
+            // Slots [wlo, whi) leave as whole words, those around them one by one.
+            const int wlo = (lo + kPerWord - 1) / kPerWord * kPerWord;
+            const int whi = hi / kPerWord * kPerWord;
+            if (wlo < whi) {
+                const bool whole = hi - lo == kStep;
+                uint32_t w[kStep][NW];
 #pragma unroll
-                    for (int d = 0; d < DV; ++d) {
-                        uint8_t* at = rows + (d * B + t) * ELEM;
+                for (int i = 0; i < kStep; ++i)
+                    if (t0 + i >= wlo && t0 + i < whi) load(t0 + i - r.off, w[i]);
+#pragma unroll
+                for (int d = 0; d < DV; ++d) {
+                    uint8_t* out = rows + (d * B + t0) * ELEM;
+                    constexpr int NX = kStep / kPerWord;
+                    uint32_t x[NX];
+#pragma unroll
+                    for (int i = 0; i < NX; ++i) {
                         if constexpr (FMT == kFmtBf16)
-                            *reinterpret_cast<uint16_t*>(at) =
-                                static_cast<uint16_t>(w[d / 2] >> (16 * (d % 2)));
+                            x[i] = __byte_perm(w[2 * i][d / 2], w[2 * i + 1][d / 2],
+                                               d % 2 ? 0x7632 : 0x5410);
                         else
-                            *at = static_cast<uint8_t>(codes2<FMT>(div(value(w, d)), 0.f));
+                            x[i] = codes4<FMT>(
+                                div(value(w[4 * i], d)), div(value(w[4 * i + 1], d)),
+                                div(value(w[4 * i + 2], d)), div(value(w[4 * i + 3], d)));
+                    }
+                    if (whole) {
+                        if constexpr (FMT == kFmtBf16)
+                            store32(out, x, p.wide_v != 0);
+                        else
+                            *reinterpret_cast<uint4*>(out) = make_uint4(x[0], x[1], x[2], x[3]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < NX; ++i)
+                            if (t0 + i * kPerWord >= wlo && t0 + i * kPerWord < whi)
+                                *reinterpret_cast<uint32_t*>(out + 4 * i) = x[i];
                     }
                 }
-                continue;
+                if (whole) continue;
             }
-            uint32_t w[kStep][NW];
+#pragma unroll 1
+            for (int t = lo; t < hi; ++t) {
+                if (t == wlo && wlo < whi) t = whi;
+                if (t >= hi) break;
+                uint32_t w[NW];
+                load(t - r.off, w);
 #pragma unroll
-            for (int i = 0; i < kStep; ++i) load(t0 + i - r.off, w[i]);
-#pragma unroll
-            for (int d = 0; d < DV; ++d) {
-                if constexpr (FMT == kFmtBf16) {
-                    uint32_t x[8];  // words of two tokens' elements of this dim
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        x[i] = __byte_perm(w[2 * i][d / 2], w[2 * i + 1][d / 2],
-                                           d % 2 ? 0x7632 : 0x5410);
-                    store32(out + d * B * 2, x, p.wide_v != 0);
-                } else {
-                    uint32_t x[4];  // words of four tokens' codes of this dim
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        x[i] = codes4<FMT>(div(value(w[4 * i], d)), div(value(w[4 * i + 1], d)),
-                                           div(value(w[4 * i + 2], d)), div(value(w[4 * i + 3], d)));
-                    *reinterpret_cast<uint4*>(out + d * B) = make_uint4(x[0], x[1], x[2], x[3]);
+                for (int d = 0; d < DV; ++d) {
+                    uint8_t* at = rows + (d * B + t) * ELEM;
+                    if constexpr (FMT == kFmtBf16)
+                        *reinterpret_cast<uint16_t*>(at) =
+                            static_cast<uint16_t>(w[d / 2] >> (16 * (d % 2)));
+                    else
+                        *at = static_cast<uint8_t>(codes2<FMT>(div(value(w, d)), 0.f));
                 }
             }
         }
