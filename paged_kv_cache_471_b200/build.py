@@ -23,7 +23,10 @@ DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(
     os.path.join(INCLUDE, "pagedattn.h")]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
-NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
+# Without unique symbols: they are one for the whole process, so that a second
+# copy of the library would take the first copy's notes of which kernels have
+# their shared-memory limit raised for its own.
+NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fno-gnu-unique",
                      "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]
 
 

@@ -2,6 +2,8 @@
 without a GPU: bad arguments are refused before any CUDA call."""
 
 import ctypes
+import shutil
+import subprocess
 
 import pytest
 
@@ -196,3 +198,14 @@ def test_decode_needs_both_scales(L, over):
                 workspace_bytes=1 << 20, stream=None)
     args.update(over)
     assert L.pa_decode(*args.values()) == pa.PA_ERR_INVALID_ARG
+
+
+@pytest.mark.skipif(shutil.which("nm") is None, reason="needs nm")
+def test_two_copies_in_one_process_share_no_state(L):
+    """A unique symbol is one for the process: a second copy of the library would believe that
+    its kernels have the shared-memory limit which the first copy raised for its own."""
+    out = subprocess.run(["nm", "-D", "--defined-only", pbuild.LIB], capture_output=True,
+                         text=True, check=True).stdout
+    names = [line.split() for line in out.splitlines()]
+    assert any(n[-1] == "pa_append_kv" for n in names)
+    assert not [n[-1] for n in names if n[-2] == "u"]
