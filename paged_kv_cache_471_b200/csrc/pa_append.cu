@@ -8,9 +8,8 @@
 // Warps share nothing and never wait for one another.  A warp takes a few rows
 // at a time in short loops -- what hides the loads' latency is many warps of
 // few registers, and straight-line code for a whole page of rows misses the
-// instruction cache (see append_keys).  A block whose scale is to be found is
-// read twice, the second time from L1; so are the rotation's table rows, by
-// each head.
+// instruction cache.  A block whose scale is to be found is read twice, the
+// second time from L1; so are the rotation's table rows, by each head.
 //
 // Bound: every row is read once and every element written once, so DRAM for
 // prompts; for single tokens the launch and two dependent rounds of loads

@@ -481,14 +481,14 @@ __global__ void __launch_bounds__(W * 32,
         const int pos0 = jg * B - (T - 1);  // ALiBi position of the stage's first slot
         if (!has_alibi) {
             if (full)
-                wa.template page<true, false>(kbase, valid, valid2, pos0, PageScales{});
+                wa.template page<true, false>(kbase, valid, valid2, pos0, PageScales{}, 0);
             else
-                wa.template page<false, false>(kbase, valid, valid2, pos0, PageScales{});
+                wa.template page<false, false>(kbase, valid, valid2, pos0, PageScales{}, 0);
         } else {
             if (full)
-                wa.template page<true, true>(kbase, valid, valid2, pos0, PageScales{});
+                wa.template page<true, true>(kbase, valid, valid2, pos0, PageScales{}, 0);
             else
-                wa.template page<false, true>(kbase, valid, valid2, pos0, PageScales{});
+                wa.template page<false, true>(kbase, valid, valid2, pos0, PageScales{}, 0);
         }
         __syncwarp();  // every lane is done with the stage before it is refilled
         --pending;

@@ -480,16 +480,8 @@ struct WarpAttn {
     // though its w vanishes in f16.  (m, l, acc) then merge as they always do.
     template <bool FULL, bool ALIBI>
     __device__ __forceinline__ void page(const uint32_t kbase, const int valid, const int valid2,
-                                         const int pos0, const PageScales& ps) {
+                                         const int pos0, const PageScales& window, const int src) {
         const uint32_t vbase = kbase + NPG * PAGE;
-        float mul[NPG], v_inv[NPG];
-        if constexpr (BLOCK) {
-#pragma unroll
-            for (int i = 0; i < NPG; ++i) {
-                mul[i] = qk_mul * ps.k[i];
-                v_inv[i] = fast_exp2(-ps.v_log2[i]);
-            }
-        }
         auto counts = [&](int tk) {  // token tk of the stage is part of the sequence
             if constexpr (PAIR) return tk < B ? tk < valid : tk - B < valid2;
             return tk < valid;
@@ -561,6 +553,19 @@ struct WarpAttn {
         }
 
         // ---------------- online softmax (log2 domain), per head row
+        // Lane `src` of the window has the stage's scales.  They are taken only now,
+        // out of the way of the logits' registers: 197.6 -> 194.4 us on 32 sequences
+        // of 4096 tokens, 32/32 heads, int8 blocks, against taking them first.
+        PageScales ps;
+        float mul[NPG], v_inv[NPG];
+        if constexpr (BLOCK) {
+            ps = shfl_page_scales(window, src, PAIR);
+#pragma unroll
+            for (int i = 0; i < NPG; ++i) {
+                mul[i] = qk_mul * ps.k[i];
+                v_inv[i] = fast_exp2(-ps.v_log2[i]);
+            }
+        }
         uint32_t pp[NH][NT];
         float alpha[NH];
         bool grew = false;
@@ -875,7 +880,7 @@ struct WarpAttnScalar {
 
     template <bool FULL, bool ALIBI>
     __device__ __forceinline__ void page(const uint32_t kbase, const int valid, const int valid2,
-                                         const int pos0, const PageScales&) {
+                                         const int pos0, const PageScales&, int) {
         const uint32_t vbase = kbase + NPG * PAGE;
         // ---------------- logits of tokens tl + 8 j (this lane's quarter of the head dims)
         float x[TJ];
@@ -1202,7 +1207,6 @@ __device__ __forceinline__ void prefix_shared_ring(const DecodeParams& p, uint32
     for (; k < span; ++k) {
         const int st = k % nsh;
         const uint32_t ph = static_cast<uint32_t>(k / nsh) & 1u;
-        PageScales ps = {};
         if constexpr (WS::BLOCK) {
             if ((k & 31) == 0) {
                 scales = load_page_scales(p.k_scale, p.v_scale, next_id, next_id2, p.num_blocks,
@@ -1210,7 +1214,6 @@ __device__ __forceinline__ void prefix_shared_ring(const DecodeParams& p, uint32
                 next_id = load_win(k + 32, 0);
                 if constexpr (PAIR) next_id2 = load_win(k + 32, 1);
             }
-            ps = shfl_page_scales(scales, k & 31, PAIR);
         }
         if (!__all_sync(kFull, mbar_wait_bounded(full0 + 8 * st, ph, p.wait_limit_ns))) {
             timed_out = true;
@@ -1223,9 +1226,9 @@ __device__ __forceinline__ void prefix_shared_ring(const DecodeParams& p, uint32
         const int valid2 = (fl & 2u) ? B : 0;
         const uint32_t kb = sbase + static_cast<uint32_t>(st * STAGE);
         if (valid == B && (!PAIR || valid2 == B))
-            wa.template page<true, false>(kb, B, B, 0, ps);
+            wa.template page<true, false>(kb, B, B, 0, scales, k & 31);
         else
-            wa.template page<false, false>(kb, valid, valid2, 0, ps);
+            wa.template page<false, false>(kb, valid, valid2, 0, scales, k & 31);
         __syncwarp();
         if (lane == 0) mbar_arrive(empty0 + 8 * st);
         if (warp == 0 && issued < span) {
@@ -1631,12 +1634,10 @@ __global__ void __launch_bounds__(W * 32,
         PageScales scales = {};
         int k = 0;
         for (; k < n_my; ++k) {
-            PageScales ps = {};
             if constexpr (WA::BLOCK) {
                 if ((k & 31) == 0)
                     scales = load_page_scales(p.k_scale, p.v_scale, win_a, win_a2, p.num_blocks,
                                               p.Hk, kvh);
-                ps = shfl_page_scales(scales, k & 31, PAIR);
             }
             const bool landed = mbar_wait_bounded(bar0 + 8 * stage, phase, p.wait_limit_ns);
             if (!__all_sync(kFull, landed)) {
@@ -1652,14 +1653,14 @@ __global__ void __launch_bounds__(W * 32,
             const int pos0 = jg * B - (T - 1);  // ALiBi position of the stage's first slot
             if (!has_alibi) {
                 if (full)
-                    wa.template page<true, false>(kbase, valid, valid2, pos0, ps);
+                    wa.template page<true, false>(kbase, valid, valid2, pos0, scales, k & 31);
                 else
-                    wa.template page<false, false>(kbase, valid, valid2, pos0, ps);
+                    wa.template page<false, false>(kbase, valid, valid2, pos0, scales, k & 31);
             } else {
                 if (full)
-                    wa.template page<true, true>(kbase, valid, valid2, pos0, ps);
+                    wa.template page<true, true>(kbase, valid, valid2, pos0, scales, k & 31);
                 else
-                    wa.template page<false, true>(kbase, valid, valid2, pos0, ps);
+                    wa.template page<false, true>(kbase, valid, valid2, pos0, scales, k & 31);
             }
             __syncwarp();
             if (k + NS < n_my) issue(k + NS);
