@@ -355,7 +355,8 @@ pa_status pa_decode_noalloc(void* out, const void* query, const void* key_cache,
  * else, the device-side checks and the errors, is as in pa_decode; a
  * query_start outside [0, num_tokens] or decreasing, or a length below n_s or
  * above the block table's, skips the sequence (PA_DEV_BAD_QUERY_START,
- * PA_DEV_SEQ_LEN_OUT_OF_RANGE).
+ * PA_DEV_SEQ_LEN_OUT_OF_RANGE), and rows of the sequences around where
+ * query_start decreases may be skipped or hold anything.
  */
 size_t pa_prefill_workspace_size(int num_tokens, int num_seqs, int num_heads, int num_kv_heads,
                                  int head_size, int block_size, int max_seq_len,
@@ -484,20 +485,22 @@ pa_status pa_copy_blocks_ex(void* key_cache, void* value_cache, float* k_scale, 
  * (query -> query_out) are rotated, values are not.
  *
  * What is stored: bf16 (round to nearest even); or e4m3 codes of x / k_scale
- * (x / v_scale for values), saturating; or, with block scales, codes of
- * x / scale[block][kv head], where the call also sets the scale: the smallest
- * power of two 2^e, -100 <= e <= 100, with |x| <= M 2^e over the call's tokens
- * in the block (M = 448 for e4m3, 127 for int8; infinities and NaNs do not
- * count), or the scale that the block has already if that is larger and the
- * run does not begin the block.  When a block's scale grows, the codes of its
+ * (x / v_scale for values), saturating, the scales being normal numbers of
+ * either sign; or, with block scales, codes of x / scale[block][kv head],
+ * where the call also sets the scale: the smallest power of two 2^e,
+ * -100 <= e <= 100, with |x| <= M 2^e over the call's tokens in the block
+ * (M = 448 for e4m3, 127 for int8; infinities and NaNs do not count), or the
+ * scale that the block has already if that is larger and the run does not
+ * begin the block.  When a block's scale grows, the codes of its
  * earlier tokens are rounded to the new scale.  A run that begins a block
  * (t mod block_size == 0) ignores the block's old scale, so blocks need no
  * clearing when they are reused.  Infinities saturate; a NaN becomes the e4m3
  * NaN, or int8 0.  Slots that the call's tokens do not fill keep their contents.
  *
  * Device data is checked as everywhere: a bad query_start or length skips the
- * sequence (PA_DEV_BAD_QUERY_START, PA_DEV_SEQ_LEN_OUT_OF_RANGE), a bad block
- * id skips the block, a position outside [0, max_position) is clamped; each
+ * sequence (PA_DEV_BAD_QUERY_START, PA_DEV_SEQ_LEN_OUT_OF_RANGE; where
+ * query_start decreases, parts of the sequences around may be skipped too), a
+ * bad block id skips the block, a position outside [0, max_position) is clamped; each
  * sets its bit in *status (a device word; may be NULL), and nothing is read or
  * written out of bounds.
  *

@@ -20,6 +20,7 @@
 #include <cstring>
 
 #include "pa_launch.cuh"
+#include "pa_query_start.cuh"
 #include "pagedattn.h"
 
 namespace pa {
@@ -589,28 +590,18 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kAppendCtasPerSm) pa_append
                (threadIdx.x >> 5);
     int s = u, a = u, b = u + 1, j = 0;
     if (p.query_start) {
+        // (Unit u looks after entry u: a bad one may leave its sequence no unit.)
+        if (task == 0 && lane == 0 && u < p.S && bad_rows(p.query_start, u, p.T))
+            flag(p, PA_DEV_BAD_QUERY_START);
         auto f = [&](int i) {
             return max(0, min(__ldg(p.query_start + i), p.T)) / B + 2 * i;
         };
-        int lo = 0, hi = p.S;
-        for (;;) {
-            const int step = (hi - lo + 31) / 32;
-            const int i = lo + lane * step;
-            const unsigned before = __ballot_sync(kFull, i < hi && f(i) <= u);
-            if (before == 0) return;  // rows before query_start[0] belong to nobody
-            lo += (__popc(before) - 1) * step;
-            hi = min(hi, lo + step);
-            if (step == 1) break;
-        }
-        s = lo;
+        s = find_sequence(p.S, lane, f, u);
+        if (s < 0 || bad_rows(p.query_start, s, p.T)) return;
         a = __ldg(p.query_start + s);
         b = __ldg(p.query_start + s + 1);
-        if (a < 0 || b < a || b > p.T) {
-            if (lane == 0) flag(p, PA_DEV_BAD_QUERY_START);
-            return;
-        }
         j = u - f(s);
-        if (a == b) return;
+        if (j < 0 || a == b) return;
     }
     const int T = __ldg(p.seq_lens + s);
     const int start = T - (b - a);  // the run's first index
@@ -623,7 +614,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kAppendCtasPerSm) pa_append
     Run r;
     r.index0 = max(start, blk * B);
     r.off = r.index0 - blk * B;
-    r.m = min(T, (blk + 1) * B) - r.index0;
+    r.m = min(T - r.index0, B - r.off);
     r.row0 = a + (r.index0 - start);
     if (task >= 2 * p.Hk) {
         if (!p.q) return;

@@ -30,6 +30,7 @@
 #include <mutex>
 
 #include "pa_launch.cuh"
+#include "pa_query_start.cuh"
 #include "pa_tcgen05.cuh"
 #include "pagedattn.h"
 
@@ -91,22 +92,6 @@ struct PrefillParams {
 struct PageMaps {
     CUtensorMap k, v;
 };
-
-// The sequence of a row or unit: the largest s in [0, S) with first(s) <= x,
-// or -1; `first` does not decrease.  A 32-way search by the whole warp.
-template <class First>
-__device__ __forceinline__ int find_sequence(int S, int lane, First first, int x) {
-    int lo = 0, hi = S;
-    for (;;) {
-        const int step = (hi - lo + 31) / 32;
-        const int i = lo + lane * step;
-        const unsigned before = __ballot_sync(kFull, i < hi && first(i) <= x);
-        if (before == 0) return -1;
-        lo += (__popc(before) - 1) * step;
-        hi = min(hi, lo + step);
-        if (step == 1) return lo;
-    }
-}
 
 template <int D, int B, bool BF16>
 struct Layout {  // shared memory, in bytes
@@ -170,16 +155,14 @@ __global__ void __launch_bounds__(cta_threads(FMT == kFmtBf16), 1)
     auto first_unit = [&](int s) {
         return max(0, min(__ldg(p.query_start + s), p.T)) / tokens_per_cta + s;
     };
+    // (Unit u looks after entry u: a bad one may leave its sequence no unit.)
+    if (rest == 0 && threadIdx.x == 0 && u < p.S && bad_rows(p.query_start, u, p.T))
+        atomicOr(p.status, PA_DEV_BAD_QUERY_START);
     const int s = find_sequence(p.S, lane, first_unit, u);
-    if (s < 0) return;
-    const int a = __ldg(p.query_start + s), b = __ldg(p.query_start + s + 1);
-    if (a < 0 || b < a || b > p.T) {
-        if (threadIdx.x == 0) atomicOr(p.status, PA_DEV_BAD_QUERY_START);
-        return;
-    }
-    const int n = b - a;
+    if (s < 0 || bad_rows(p.query_start, s, p.T)) return;
+    const int a = __ldg(p.query_start + s), n = __ldg(p.query_start + s + 1) - a;
     const int tok0 = (u - first_unit(s)) * tokens_per_cta;  // first query token of the CTA
-    if (tok0 >= n) return;
+    if (tok0 < 0 || tok0 >= n) return;
     const int T = __ldg(p.seq_lens + s);
     if (T < n || T > static_cast<long long>(p.max_blocks) * B) {
         if (threadIdx.x == 0) atomicOr(p.status, PA_DEV_SEQ_LEN_OUT_OF_RANGE);
@@ -187,14 +170,17 @@ __global__ void __launch_bounds__(cta_threads(FMT == kFmtBf16), 1)
     }
     // Query token i sees the keys [0, T - n + i].  Key tiles of this partition,
     // for each row tile: [j0, j0 + count(t)).
+    // (Sums with a length that reaches 2^31 - 1 stay below it.)
     const int seen0 = T - n + tok0 + 1;                                  // by the first row
-    const int seen_end = min(T, seen0 + tokens_per_cta - 1);             // by the last
+    auto seen_by = [&](int i) { return seen0 + min(T - seen0, i); };     // by i tokens later
+    const int seen_end = seen_by(tokens_per_cta - 1);                    // by the last
+    const int pages = (seen_end - 1) / B + 1;
     const int j0 = part * p.tiles_per_part;
     auto count = [&](int t) {
         if (tok0 + t * p.tokens_per_tile >= n) return 0;
-        const int seen = min(T, seen0 + (t + 1) * p.tokens_per_tile - 1);
+        const int seen = seen_by((t + 1) * p.tokens_per_tile - 1);
         // (The last partition takes all that is left, also behind max_seq_len.)
-        const int tiles = (seen + kKeys - 1) / kKeys - j0;
+        const int tiles = (seen - 1) / kKeys + 1 - j0;
         return max(0, part == p.P - 1 ? tiles : min(tiles, p.tiles_per_part));
     };
     const int n0 = count(0), n1 = count(1);
@@ -252,7 +238,7 @@ __global__ void __launch_bounds__(cta_threads(FMT == kFmtBf16), 1)
         // Lane l < NPG: the id of page l of key tile j (-1: none, or not legal).
         auto page_id = [&](int j) {
             const int pg = (j0 + j) * NPG + lane;
-            if (lane >= NPG || j >= steps || pg * B >= seen_end) return -1;
+            if (lane >= NPG || j >= steps || pg >= pages) return -1;
             const int id = __ldg(btrow + pg);
             if (id >= 0 && id < p.num_blocks) return id;
             atomicOr(p.status, PA_DEV_BAD_BLOCK_ID);
@@ -343,7 +329,7 @@ __global__ void __launch_bounds__(cta_threads(FMT == kFmtBf16), 1)
             if (lane == 0) mbar_arrive(i_full + 8 * (j % kInfo));
         };
         // Tiles with keys that some row does not see.
-        auto edge = [&](int j) { return (j0 + j + 1) * kKeys > seen0; };
+        auto edge = [&](int j) { return j0 + j >= seen0 / kKeys; };
         if constexpr (BF16) {
             // K: a gather of four pages brings one 16-byte column of each (B
             // tokens of 8 head dims) to consecutive addresses of the tile's
@@ -890,10 +876,10 @@ __global__ void __launch_bounds__(kThreads)
         const int token = static_cast<int>(row / p.Hq);
         const int s = find_sequence(
             p.S, lane, [&](int i) { return max(0, min(__ldg(p.query_start + i), p.T)); }, token);
-        if (s < 0) return {-1, row};
+        if (s < 0 || bad_rows(p.query_start, s, p.T)) return {-1, row};
         const int a = __ldg(p.query_start + s), b = __ldg(p.query_start + s + 1);
         const int len = __ldg(p.seq_lens + s);
-        const bool mine = a >= 0 && b <= p.T && token >= a && token < b && len >= b - a &&
+        const bool mine = token >= a && token < b && len >= b - a &&
                           len <= static_cast<long long>(p.max_blocks) * block_size;
         return {mine ? p.P : -1, row};
     });
@@ -1086,8 +1072,7 @@ extern "C" pa_status pa_prefill(void* out, const void* query, const void* key_ca
     if (static_cast<long long>(max_seq_len) >
         static_cast<long long>(max_blocks_per_seq) * block_size)
         return fail(PA_ERR_INVALID_ARG, "%s", "max_seq_len > max_blocks_per_seq * block_size");
-    if (num_blocks < 1 || num_blocks * num_kv_heads > 0x7ffffffeLL ||
-        num_blocks > 0x7ffffffeLL)
+    if (num_blocks < 1 || num_blocks > 0x7ffffffeLL / num_kv_heads)
         return fail(PA_ERR_INVALID_ARG, "%s",
                     "num_blocks and num_blocks * num_kv_heads must be in [1, 2^31 - 1)");
     if (num_tokens == 0 || num_seqs == 0) return PA_OK;

@@ -285,6 +285,41 @@ def test_bad_device_data_is_flagged_and_skipped():
         once(lambda c, s: s.__setitem__(i, x), pa.PA_DEV_BAD_QUERY_START)
 
 
+# Prefix sums that decrease somewhere: the first has a unit whose search ends at
+# sequence 1, which begins behind that unit.
+DECREASING = [[0, 100, 120, 5, 200], [0, 190, 200, 3, 3], [150, 160, 20, 180, 190],
+              [0, 64, 64, 32, 200], [0, 200, 0, 200, 0]]
+
+
+@pytest.mark.parametrize("ends", DECREASING)
+@pytest.mark.parametrize("kv", ["bf16", "int8_block"])
+def test_a_decreasing_query_start_writes_nothing_out_of_place(kv, ends):
+    S, B, D, raw = 4, 16, 64, Cache._raw
+    cache, _, host, parts, angles = make(kv, [200] * S, [9] * S, 1, 1, D, B, D)
+    kc, vc = cache.packed(DEV)
+    ks, vs = cache.scales(DEV)
+    rows = {n: t[:200].contiguous() for n, t in parts.items()}
+    before = cache.unpacked(kc, vc)
+    pa.read_status(device=DEV, clear=True)
+    pa.append_kv(kc, vc, rows["key"], rows["value"], cache.tables.to(DEV), cache.lens.to(DEV), B,
+                 kv, ks, vs, query_start=torch.tensor(ends, dtype=torch.int32, device=DEV),
+                 cos_sin=angles.to(DEV), query=rows["query"])
+    torch.cuda.synchronize()
+    assert pa.read_status(device=DEV, clear=True) & pa.PA_DEV_BAD_QUERY_START
+    for was, now in zip(before, cache.unpacked(kc, vc)):
+        for blk in range(was.shape[0]):
+            keep = slice(0, B)
+            for s in range(S):
+                at = (cache.tables[s] == blk).nonzero()
+                n = ends[s + 1] - ends[s]
+                if len(at) and 0 <= n <= 200:
+                    # its last n tokens may have been written (and the tokens before
+                    # them in a block, to the block's new scale)
+                    first = max(0, min(B, int(cache.lens[s]) - n - int(at[0]) * B))
+                    keep = slice(0, 0 if is_block(kv) and first < B else first)
+            assert same(raw(was)[blk, :, keep], raw(now)[blk, :, keep]), (blk, keep)
+
+
 @pytest.mark.parametrize("kv", ["bf16", "int8_block"])
 def test_blocks_past_4_gib(kv):
     """Offsets past 32 bits."""

@@ -218,6 +218,29 @@ def test_bad_device_data_is_flagged_and_skipped():
         assert ((out[:20].cpu().double() - ref[:20]).abs() <= tol[:20]).all()
 
 
+@pytest.mark.parametrize("pages", [0, 8])
+@pytest.mark.parametrize("at", [[0, 100, 120, 5, 200], [0, 190, 200, 3, 3],
+                                [150, 160, 20, 180, 190], [0, 64, 64, 32, 200],
+                                [0, 200, 0, 200, 0], [0, 200, 199, 200, 1]])
+def test_a_decreasing_query_start_stays_in_bounds(at, pages):
+    """Flagged, and nothing is written but the rows of a sequence's legal range."""
+    cache = Cache("fp8_e4m3", [230] * 4, 1, 64, 16, seed=12)
+    room = torch.full((600, 1, 64), float("nan"), dtype=torch.bfloat16, device=DEV)
+    kc, vc = cache.packed(DEV)
+    ks, vs = cache.scales(DEV)
+    pa.read_status(device=DEV, clear=True)
+    pa.prefill(room[200:400], queries(200, 1, 64).to(DEV), kc, vc, 1, 0.125,
+               cache.tables.to(DEV), cache.lens.to(DEV),
+               torch.tensor(at, dtype=torch.int32, device=DEV), 16, 240, "fp8_e4m3", ks, vs,
+               partition_pages=pages)
+    torch.cuda.synchronize()
+    assert pa.read_status(device=DEV, clear=True) == pa.PA_DEV_BAD_QUERY_START
+    owned = torch.zeros(600, dtype=torch.bool)
+    for a, b in zip(at, at[1:]):
+        owned[200 + a:200 + max(a, b)] = True
+    assert torch.isnan(room.float().cpu()[~owned]).all()
+
+
 def test_many_sequences_and_blocks_past_4_gib():
     S = 700
     new = [(i * 7) % 4 for i in range(S)]
