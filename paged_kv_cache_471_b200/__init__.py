@@ -270,7 +270,8 @@ def workspace(nbytes: int, device, stream=None):
     if dev.index is None:
         dev = torch.device(dev.type, torch.cuda.current_device())
     nbytes = max(nbytes, WORKSPACE_HEADER_BYTES)
-    capturing = torch.cuda.is_current_stream_capturing()
+    with _NO_CHANGE if stream is None else torch.cuda.stream(stream):
+        capturing = torch.cuda.is_current_stream_capturing()
     key = (dev.index, _stream_ptr(stream, dev))
     ws = _ws_cache.get(key)
     if not capturing and ws is not None and ws.numel() >= nbytes:
@@ -530,8 +531,9 @@ def read_status(workspace_tensor=None, device=None, clear=False, stream=None) ->
         dev = torch.device(device) if device is not None else torch.device("cuda")
         if dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
-        words = [ws for key, ws in _ws_cache.items() if key[0] == dev.index]
-        words += [w for index, w in _status_words.items() if index == dev.index]
+        words = [ws for key, ws in list(_ws_cache.items()) if key[0] == dev.index]
+        if dev.index in _status_words:
+            words.append(_status_words[dev.index])
         if words:  # calls of other streams may still be running
             torch.cuda.synchronize(dev)
     st = stream if stream is not None else torch.cuda.current_stream(dev)
@@ -704,7 +706,7 @@ def append_kv(key_cache, value_cache, key, value, block_tables, seq_lens, block_
     code = kv_dtype_code(kv_dtype)
     dev = key_cache.device
     kv_types = _kv_types(code)
-    int32 = (torch.int32,)
+    int32, words = (torch.int32,), (torch.int32, torch.uint32)
     kc = _ptr(key_cache, "key_cache", kv_types, dev)
     vc = _ptr(value_cache, "value_cache", kv_types, dev)
     if key_cache.dim() != 5 or value_cache.dim() != 4:
@@ -757,7 +759,7 @@ def append_kv(key_cache, value_cache, key, value, block_tables, seq_lens, block_
         word = _status_word(dev) if status is None else status
         rc = lib().pa_append_kv(kc, vc, k, v, T, S, Hk, D, bt, block_tables.shape[1], sl, qs, B,
                                 num_blocks, code, ks, vs,
-                                None if word is None else _ptr(word, "status", None, dev),
+                                None if word is None else _ptr(word, "status", words, dev),
                                 _stream_ptr(stream, dev), ctypes.byref(o))
     _check(rc)
     return query_out

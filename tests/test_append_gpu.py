@@ -422,6 +422,8 @@ def test_binding_refusals():
     refused(TypeError, kv_dtype="int8_block")
     refused(ValueError, query_start=start.to(DEV)[:-1])
     refused(ValueError, key_cache=kc[:2])
+    refused(TypeError, status=torch.zeros(4, dtype=torch.uint8, device=DEV))
+    refused(ValueError, status=torch.zeros(1, dtype=torch.int32))
     odd = torch.zeros(7 * 130, dtype=torch.bfloat16, device=DEV).as_strided((7, 2, 64), (130, 64, 1))
     refused(pa.PagedAttentionError, key=odd)  # a row stride that is no multiple of 8
     pa.append_kv(**base)
