@@ -1,4 +1,5 @@
-"""Python binding of libpagedattn (paged decode attention, B200 / sm_100a).
+"""Python binding of libpagedattn (a paged KV cache and the attention over it,
+B200 / sm_100a).
 
 Argument marshalling only: every step of the computation runs in the CUDA
 kernels of ``libpagedattn.so``; torch is used for device memory and streams.
@@ -8,6 +9,8 @@ If the library has not been built the calls raise -- there is no fallback.
 #47361 benchmark snippet (out, query, key_cache, value_cache, num_kv_heads,
 scale, block_tables, seq_lens, block_size, max_seq_len, kv dtype, k_scale,
 v_scale), with the split-KV temporaries folded into one optional workspace.
+``append_kv`` writes tokens into the cache, ``prefill`` is attention for many
+query tokens of a sequence; both take the cache as ``decode`` does.
 """
 
 from __future__ import annotations

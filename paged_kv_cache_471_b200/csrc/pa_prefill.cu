@@ -5,12 +5,13 @@
 // One CTA per (group of query tokens, kv head, key partition).  Its rows are
 // (query token, head of the kv head's group) pairs, tokens slowest, in two
 // tiles of 128 rows; key tiles of 128 tokens pass by once for all 256 rows:
-//   * warps 8 and 9 gather the tile's pages into shared memory as tensor-core
-//     operands.  Both page layouts are K-major already (K: 16-byte columns of 8
-//     head dims; V: rows of B tokens), so bulk and TMA copies put bf16 pages in
-//     place without a register; 8-bit codes are widened to f16 (exact) on the way;
-//   * warp 10 issues the products: S = Q K^T into TMEM, then O += P V with P
-//     read from TMEM, where it lies over the S it came from;
+//   * the loader warps, from 8 on, gather the tile's pages into shared memory as
+//     tensor-core operands.  Both page layouts are K-major already (K: 16-byte
+//     columns of 8 head dims; V: rows of B tokens), so two warps' TMA copies put
+//     bf16 pages in place without a register; 8-bit codes are widened to f16
+//     (exact) on the way, by three warps;
+//   * the warp after them issues the products: S = Q K^T into TMEM, then O += P V
+//     with P read from TMEM, where it lies over the S it came from;
 //   * warps 0-3 and 4-7 hold a row of one tile per thread: the running maximum
 //     and sum, P = 2^(x - m) back to TMEM.  While one tile is in softmax, the
 //     tensor cores work on the other's products.
@@ -19,7 +20,15 @@
 // carry at the same relative precision.
 //
 // Bound: 4 D flops per (row, key) on the tensor cores, against one exponential
-// per (row, key): 16 a clock and SM, so at D = 128 both need the same time.
+// per (row, key): 16 a clock and SM, so at D = 128 both need the same time, 2048
+// clocks a step of the 256 rows.  A step takes 3500, 4000 when a row rescales: a
+// tile's chain of softmax (1980: scores loaded 240, maximum 350, weights 1390),
+// hand-overs (620) and its own products.  Measured, D = 128:
+//   1 prompt of 8192 tokens, 32/8 heads, bf16        570-620 us, 890-965 TFLOP/s
+//   4 chunks of 257-1025 tokens behind up to 4001,
+//   64/8 heads, e4m3 blocks                          352 us, 675 TFLOP/s
+// (the first at the card's power limit).  Part of the exponentials as a
+// polynomial on the FMA pipes made it slower: a quarter of them 671, half 732 us.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
