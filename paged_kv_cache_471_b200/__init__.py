@@ -15,7 +15,6 @@ query tokens of a sequence; both take the cache as ``decode`` does.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 import os
@@ -232,9 +231,9 @@ def _prefill_workspace_size(device, *args):
 
 
 @functools.lru_cache(maxsize=4096)
-def _workspace_size(device, *args, **kw):
+def _workspace_size(device, *args):
     """workspace_size for the current device (number `device`)."""
-    return workspace_size(*args, **kw)
+    return workspace_size(*args)
 
 
 def workspace_size(num_seqs, num_heads, num_kv_heads, head_size, block_size, max_seq_len,
@@ -253,12 +252,27 @@ _ws_cache = {}
 _status_words = {}
 
 
-def _stream_ptr(stream, dev):
-    """The cudaStream_t of a call: the given stream's, or the current one's."""
+@functools.lru_cache(maxsize=None)
+def _torch():
+    """torch, which is imported by the first call, and the types that calls check."""
+    import torch
+    return torch, (torch.bfloat16,), (torch.float32,), (torch.int32,)
+
+
+def _stream_ptr(stream, index):
+    """The cudaStream_t of a call: the given stream's, or the current one's of
+    device number `index`."""
     if stream is not None:
         return stream.cuda_stream
-    import torch
-    return torch._C._cuda_getCurrentRawStream(dev.index)
+    return _torch()[0]._C._cuda_getCurrentRawStream(index)
+
+
+def _capturing(stream):
+    torch = _torch()[0]
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
 
 
 def workspace(nbytes: int, device, stream=None):
@@ -268,21 +282,24 @@ def workspace(nbytes: int, device, stream=None):
     so each stream has its own.  While the stream is being captured into a
     graph, the workspace is a new one that belongs to the graph alone and is
     zeroed by each replay."""
-    import torch
+    torch = _torch()[0]
     dev = torch.device(device)
-    if dev.index is None:
-        dev = torch.device(dev.type, torch.cuda.current_device())
-    nbytes = max(nbytes, WORKSPACE_HEADER_BYTES)
-    with _NO_CHANGE if stream is None else torch.cuda.stream(stream):
-        capturing = torch.cuda.is_current_stream_capturing()
-    key = (dev.index, _stream_ptr(stream, dev))
+    index = torch.cuda.current_device() if dev.index is None else dev.index
+    return _workspace(max(nbytes, WORKSPACE_HEADER_BYTES), index, stream)
+
+
+def _workspace(nbytes, index, stream):
+    """workspace for device number `index`."""
+    torch = _torch()[0]
+    capturing = _capturing(stream)
+    key = (index, _stream_ptr(stream, index))
     ws = _ws_cache.get(key)
     if not capturing and ws is not None and ws.numel() >= nbytes:
         return ws
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
+        stream = torch.cuda.current_stream(index)
     with torch.cuda.stream(stream):  # zeroed, and later freed, in that stream's order
-        new = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+        new = torch.zeros(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
         if capturing:
             return new
         if ws is not None:  # keep the status bits
@@ -291,53 +308,59 @@ def workspace(nbytes: int, device, stream=None):
     return new
 
 
-def _status_word(dev):
+def _status_word(index):
     """The device word that append_kv reports to by default; read_status reads
     it with the workspaces'.  None while capturing if no call made it before."""
-    import torch
-    word = _status_words.get(dev.index)
+    word = _status_words.get(index)
     if word is None:
+        torch = _torch()[0]
         if torch.cuda.is_current_stream_capturing():
             return None
-        word = torch.zeros(4, dtype=torch.int32, device=dev)
-        torch.cuda.synchronize(dev)  # once per device: zeroed before any stream's call
-        _status_words[dev.index] = word
+        word = torch.zeros(4, dtype=torch.int32, device=torch.device("cuda", index))
+        torch.cuda.synchronize(index)  # once per device: zeroed before any stream's call
+        _status_words[index] = word
     return word
 
 
-_NO_CHANGE = contextlib.nullcontext()
+def _enter_device(index):
+    """Make device number `index` the current one, which the library plans for
+    and launches on; returns the one to go back to, or None."""
+    torch = _torch()[0]
+    now = torch._C._cuda_getDevice()
+    if now == index:
+        return None
+    torch.cuda.set_device(index)
+    return now
 
 
-def _on_device(dev):
-    """The library launches on the current device: make it `dev`."""
-    import torch
-    if torch.cuda.current_device() == dev.index:
-        return _NO_CHANGE
-    return torch.cuda.device(dev)
+def _leave_device(previous):
+    if previous is not None:
+        _torch()[0].cuda.set_device(previous)
 
 
-def _refuse(t, name, dtypes, device):
+def _refuse(t, name, dtypes, index):
     """Raise for what _ptr found wrong."""
-    import torch
+    torch = _torch()[0]
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected device {index}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
 
 
-def _ptr(t, name, dtypes=None, device=None):
+def _ptr(t, name, dtypes, index):
+    """The address of a contiguous CUDA tensor on device number `index`."""
     try:
-        if (t.is_cuda and (device is None or t.device == device) and t.is_contiguous()
-                and (dtypes is None or t.dtype in dtypes)):
+        if t.get_device() == index >= 0 and t.is_contiguous() \
+                and (dtypes is None or t.dtype in dtypes):
             return t.data_ptr()
     except AttributeError:
         pass
-    return _refuse(t, name, dtypes, device)
+    return _refuse(t, name, dtypes, index)
 
 
 @functools.lru_cache(maxsize=None)
@@ -350,13 +373,12 @@ def _kv_types(code):
     return (torch.uint8, torch.float8_e4m3fn)
 
 
-def _scale_ptrs(code, k_scale, v_scale, num_blocks, num_kv_heads, dev):
+def _scale_ptrs(code, k_scale, v_scale, num_blocks, num_kv_heads, index):
     """Pointers to the scales of an 8-bit cache (None, None for bf16)."""
-    import torch
     if code == PA_KV_BF16:
         return None, None
-    ptrs = (_ptr(k_scale, "k_scale", (torch.float32,), dev),
-            _ptr(v_scale, "v_scale", (torch.float32,), dev))
+    f32 = _torch()[2]
+    ptrs = _ptr(k_scale, "k_scale", f32, index), _ptr(v_scale, "v_scale", f32, index)
     if code != PA_KV_FP8_E4M3:
         for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
             if t.shape != (num_blocks, num_kv_heads):
@@ -388,55 +410,49 @@ def decode(out, query, key_cache, value_cache, num_kv_heads: int, scale: float, 
     defaults to a cached zeroed buffer per device and stream; stream defaults
     to the current stream.
     """
-    import torch
+    _, bf16, f32, i32 = _torch()
     code = kv_dtype_code(kv_dtype)
-    dev = query.device
+    index = query.get_device()
     S, Hq, D = query.shape
     kv_types = _kv_types(code)
-    args_ptrs = [
-        _ptr(out, "out", (torch.bfloat16,), dev),
-        _ptr(query, "query", (torch.bfloat16,), dev),
-        _ptr(key_cache, "key_cache", kv_types, dev),
-        _ptr(value_cache, "value_cache", kv_types, dev),
-    ]
-    if tuple(out.shape) != (S, Hq, D):
+    ptrs = (_ptr(out, "out", bf16, index), _ptr(query, "query", bf16, index),
+            _ptr(key_cache, "key_cache", kv_types, index),
+            _ptr(value_cache, "value_cache", kv_types, index))
+    if out.shape != query.shape:
         raise ValueError("out must have the query's shape")
     if key_cache.dim() != 5 or value_cache.dim() != 4:
         raise ValueError("key_cache must be 5-D and value_cache 4-D")
-    num_blocks = key_cache.shape[0]
-    if value_cache.shape[0] != num_blocks or key_cache.shape[3] != block_size \
-            or value_cache.shape[3] != block_size or key_cache.shape[1] != num_kv_heads \
-            or value_cache.shape[1] != num_kv_heads or value_cache.shape[2] != D \
-            or key_cache.shape[2] * key_cache.shape[4] != D:
+    num_blocks, k_heads, groups, k_block, x = key_cache.shape
+    if value_cache.shape != (num_blocks, num_kv_heads, D, block_size) \
+            or k_heads != num_kv_heads or k_block != block_size or groups * x != D:
         raise ValueError("cache shapes do not match query / num_kv_heads / block_size")
-    bt = _ptr(block_tables, "block_tables", (torch.int32,), dev)
-    sl = _ptr(seq_lens, "seq_lens", (torch.int32,), dev)
-    if block_tables.dim() != 2 or block_tables.shape[0] != S or seq_lens.shape != (S,):
+    bt = _ptr(block_tables, "block_tables", i32, index)
+    sl = _ptr(seq_lens, "seq_lens", i32, index)
+    tables = block_tables.shape
+    if len(tables) != 2 or tables[0] != S or seq_lens.shape != (S,):
         raise ValueError("block_tables must be [num_seqs, max_blocks] and seq_lens [num_seqs]")
-    ks, vs = _scale_ptrs(code, k_scale, v_scale, num_blocks, num_kv_heads, dev)
+    ks, vs = _scale_ptrs(code, k_scale, v_scale, num_blocks, num_kv_heads, index)
     alibi = None
     if alibi_slopes is not None:
         if alibi_slopes.shape != (Hq,):
             raise ValueError("alibi_slopes must be [num_heads]")
-        alibi = _ptr(alibi_slopes, "alibi_slopes", (torch.float32,), dev)
-    # The library plans for, and launches on, the current device: make it the
-    # tensors' device for the call.
-    with _on_device(dev):
+        alibi = _ptr(alibi_slopes, "alibi_slopes", f32, index)
+    previous = _enter_device(index)
+    try:
         if workspace_tensor is None:  # (a given one is size-checked by the library)
-            need = _workspace_size(dev.index, S, Hq, num_kv_heads, D, block_size, max_seq_len,
-                                   code, partition_pages,
-                                   shared_prefix_blocks=shared_prefix_blocks,
-                                   fp8_compute=bool(fp8_compute) and code == PA_KV_FP8_E4M3,
-                                   schedule=schedule, stages=stages, num_sms=num_sms)
-            workspace_tensor = workspace(need, dev, stream)
-        ws = _ptr(workspace_tensor, "workspace", None, dev)
-        rc = lib().pa_decode_ex(*args_ptrs, S, Hq, int(num_kv_heads), D, float(scale), bt,
-                                block_tables.shape[1], sl, int(block_size), int(max_seq_len),
-                                int(num_blocks), code, ks, vs, ws,
-                                workspace_tensor.numel() * workspace_tensor.element_size(),
-                                _stream_ptr(stream, dev),
+            need = _workspace_size(index, S, Hq, num_kv_heads, D, block_size, max_seq_len, code,
+                                   partition_pages, num_sms, shared_prefix_blocks,
+                                   bool(fp8_compute) and code == PA_KV_FP8_E4M3, schedule, stages)
+            workspace_tensor = _workspace(need, index, stream)
+        ws = _ptr(workspace_tensor, "workspace", None, index)
+        rc = lib().pa_decode_ex(*ptrs, S, Hq, int(num_kv_heads), D, float(scale), bt, tables[1],
+                                sl, int(block_size), int(max_seq_len), num_blocks, code, ks, vs,
+                                ws, workspace_tensor.numel() * workspace_tensor.element_size(),
+                                _stream_ptr(stream, index),
                                 _opts(partition_pages, num_sms, stages, shared_prefix_blocks, alibi,
                                       fp8_compute, test_stall_copies, schedule, mha_cuda_cores))
+    finally:
+        _leave_device(previous)
     _check(rc)
     return out
 
@@ -456,41 +472,43 @@ def prefill(out, query, key_cache, value_cache, num_kv_heads: int, scale: float,
     partition_pages > 0 forces a split of the keys into partitions of that many
     blocks (by default only batches with few rows are split).
     """
-    import torch
+    _, bf16, _, i32 = _torch()
     code = kv_dtype_code(kv_dtype)
-    dev = query.device
+    index = query.get_device()
     kv_types = _kv_types(code)
     T, Hq, D = query.shape
-    ptrs = (_ptr(out, "out", (torch.bfloat16,), dev), _ptr(query, "query", (torch.bfloat16,), dev),
-            _ptr(key_cache, "key_cache", kv_types, dev),
-            _ptr(value_cache, "value_cache", kv_types, dev))
+    ptrs = (_ptr(out, "out", bf16, index), _ptr(query, "query", bf16, index),
+            _ptr(key_cache, "key_cache", kv_types, index),
+            _ptr(value_cache, "value_cache", kv_types, index))
     if out.shape != query.shape:
         raise ValueError("out must have the query's shape")
     num_blocks, x = key_cache.shape[0], 16 // key_cache.element_size()
     if key_cache.shape != (num_blocks, num_kv_heads, D // x, block_size, x) \
             or value_cache.shape != (num_blocks, num_kv_heads, D, block_size):
         raise ValueError("cache shapes do not match query / num_kv_heads / block_size")
-    bt = _ptr(block_tables, "block_tables", (torch.int32,), dev)
-    sl = _ptr(seq_lens, "seq_lens", (torch.int32,), dev)
-    qs = _ptr(query_start, "query_start", (torch.int32,), dev)
-    if seq_lens.dim() != 1 or block_tables.dim() != 2 \
-            or block_tables.shape[0] != seq_lens.shape[0] \
-            or query_start.shape != (seq_lens.shape[0] + 1,):
+    bt = _ptr(block_tables, "block_tables", i32, index)
+    sl = _ptr(seq_lens, "seq_lens", i32, index)
+    qs = _ptr(query_start, "query_start", i32, index)
+    tables = block_tables.shape
+    if seq_lens.dim() != 1 or len(tables) != 2 or tables[0] != seq_lens.shape[0] \
+            or query_start.shape != (tables[0] + 1,):
         raise ValueError("block_tables must be [num_seqs, max_blocks], seq_lens [num_seqs] and "
                          "query_start [num_seqs + 1]")
-    S = seq_lens.shape[0]
-    ks, vs = _scale_ptrs(code, k_scale, v_scale, num_blocks, num_kv_heads, dev)
-    with _on_device(dev):
+    S = tables[0]
+    ks, vs = _scale_ptrs(code, k_scale, v_scale, num_blocks, num_kv_heads, index)
+    previous = _enter_device(index)
+    try:
         if workspace_tensor is None:  # (a given one is size-checked by the library)
-            need = _prefill_workspace_size(dev.index, T, S, Hq, num_kv_heads, D, block_size,
+            need = _prefill_workspace_size(index, T, S, Hq, num_kv_heads, D, block_size,
                                            max_seq_len, code, partition_pages, num_sms)
-            workspace_tensor = workspace(need, dev, stream)
-        rc = lib().pa_prefill(*ptrs, T, S, Hq, int(num_kv_heads), D, float(scale), bt,
-                              block_tables.shape[1], sl, qs, int(block_size), int(max_seq_len),
-                              num_blocks, code, ks, vs,
-                              _ptr(workspace_tensor, "workspace", None, dev),
-                              workspace_tensor.numel() * workspace_tensor.element_size(),
-                              _stream_ptr(stream, dev), _opts(partition_pages, num_sms))
+            workspace_tensor = _workspace(need, index, stream)
+        ws = _ptr(workspace_tensor, "workspace", None, index)
+        rc = lib().pa_prefill(*ptrs, T, S, Hq, int(num_kv_heads), D, float(scale), bt, tables[1],
+                              sl, qs, int(block_size), int(max_seq_len), num_blocks, code, ks, vs,
+                              ws, workspace_tensor.numel() * workspace_tensor.element_size(),
+                              _stream_ptr(stream, index), _opts(partition_pages, num_sms))
+    finally:
+        _leave_device(previous)
     _check(rc)
     return out
 
@@ -503,18 +521,18 @@ def decode_noalloc(out, query, key_cache, value_cache, num_kv_heads: int, scale:
     (NOALLOC_SCRATCH_BYTES per GPU), so nothing is allocated here.  Calls that
     overlap on the GPU share that array and must be serialised by the caller;
     the first call on a device should come before any stream capture."""
-    import torch
+    torch, bf16, _, i32 = _torch()
     code = kv_dtype_code(kv_dtype)
-    dev = query.device
+    dev, index = query.device, query.get_device()
     S, Hq, D = query.shape
     kv_types = _kv_types(code)
-    ks, vs = _scale_ptrs(code, k_scale, v_scale, key_cache.shape[0], num_kv_heads, dev)
+    ks, vs = _scale_ptrs(code, k_scale, v_scale, key_cache.shape[0], num_kv_heads, index)
     st = stream if stream is not None else torch.cuda.current_stream(dev)
-    ptrs = (_ptr(out, "out", (torch.bfloat16,), dev), _ptr(query, "query", (torch.bfloat16,), dev),
-            _ptr(key_cache, "key_cache", kv_types, dev),
-            _ptr(value_cache, "value_cache", kv_types, dev))
-    bt = _ptr(block_tables, "block_tables", (torch.int32,), dev)
-    sl = _ptr(seq_lens, "seq_lens", (torch.int32,), dev)
+    ptrs = (_ptr(out, "out", bf16, index), _ptr(query, "query", bf16, index),
+            _ptr(key_cache, "key_cache", kv_types, index),
+            _ptr(value_cache, "value_cache", kv_types, index))
+    bt = _ptr(block_tables, "block_tables", i32, index)
+    sl = _ptr(seq_lens, "seq_lens", i32, index)
     with torch.cuda.device(dev):  # the scratch array of the tensors' device
         rc = lib().pa_decode_noalloc(*ptrs, S, Hq, int(num_kv_heads), D, float(scale), bt,
                                      block_tables.shape[1], sl, int(block_size), int(max_seq_len),
@@ -636,7 +654,7 @@ def copy_blocks(key_cache, value_cache, src, dst, kv_dtype="bf16", status=None, 
     copied with the blocks."""
     import torch
     code = kv_dtype_code(kv_dtype)
-    dev = key_cache.device
+    dev, index = key_cache.device, key_cache.get_device()
     kv_types = _kv_types(code)
     n = int(src.numel())
     if int(dst.numel()) != n:
@@ -645,27 +663,26 @@ def copy_blocks(key_cache, value_cache, src, dst, kv_dtype="bf16", status=None, 
     st = stream if stream is not None else torch.cuda.current_stream(dev)
     ks = vs = None
     if code in (PA_KV_FP8_E4M3_BLOCK, PA_KV_INT8_BLOCK):
-        ks, vs = _scale_ptrs(code, k_scale, v_scale, key_cache.shape[0], Hk, dev)
-    args = (_ptr(key_cache, "key_cache", kv_types, dev),
-            _ptr(value_cache, "value_cache", kv_types, dev), ks, vs,
+        ks, vs = _scale_ptrs(code, k_scale, v_scale, key_cache.shape[0], Hk, index)
+    args = (_ptr(key_cache, "key_cache", kv_types, index),
+            _ptr(value_cache, "value_cache", kv_types, index), ks, vs,
             int(Hk), int(D), int(value_cache.shape[3]), int(key_cache.shape[0]), code,
-            _ptr(src, "src", (torch.int64,), dev), _ptr(dst, "dst", (torch.int64,), dev), n,
-            None if status is None else _ptr(status, "status", None, dev), st.cuda_stream)
+            _ptr(src, "src", (torch.int64,), index), _ptr(dst, "dst", (torch.int64,), index), n,
+            None if status is None else _ptr(status, "status", None, index), st.cuda_stream)
     with torch.cuda.device(dev):
         rc = lib().pa_copy_blocks_ex(*args)
     _bm_check(rc)
 
 
 # ------------------------------------------------------------- appending tokens
-def _rows(t, name, tokens, heads, head_size, dev):
+def _rows(t, name, tokens, heads, head_size, index):
     """Pointer and row stride of a bf16 [tokens, heads, head_size] tensor whose
     heads are dense (a view of a wider projection's output will do)."""
-    import torch
     try:
-        if t.dtype != torch.bfloat16 or t.device != dev:
-            _refuse(t, name, (torch.bfloat16,), dev)
+        if t.get_device() != index or t.dtype not in _torch()[1]:
+            _refuse(t, name, _torch()[1], index)
     except AttributeError:
-        _refuse(t, name, None, dev)
+        _refuse(t, name, None, index)
     if t.shape != (tokens, heads, head_size):
         raise ValueError(f"{name} must be [{tokens}, {heads}, {head_size}]")
     if tokens == 0:
@@ -705,43 +722,42 @@ def append_kv(key_cache, value_cache, key, value, block_tables, seq_lens, block_
     int32 / uint32 CUDA word for the PA_DEV_* bits (default: one that
     read_status reads).  Returns query_out (None without a query).
     """
-    import torch
+    torch, _, f32, int32 = _torch()
     code = kv_dtype_code(kv_dtype)
-    dev = key_cache.device
+    index = key_cache.get_device()
     kv_types = _kv_types(code)
-    int32, words = (torch.int32,), (torch.int32, torch.uint32)
-    kc = _ptr(key_cache, "key_cache", kv_types, dev)
-    vc = _ptr(value_cache, "value_cache", kv_types, dev)
+    kc = _ptr(key_cache, "key_cache", kv_types, index)
+    vc = _ptr(value_cache, "value_cache", kv_types, index)
     if key_cache.dim() != 5 or value_cache.dim() != 4:
         raise ValueError("key_cache must be 5-D and value_cache 4-D")
     num_blocks, Hk, D, B = value_cache.shape
     x = 8 if code == PA_KV_BF16 else 16
     if B != block_size or key_cache.shape != (num_blocks, Hk, D // x, B, x):
         raise ValueError("cache shapes do not match each other / block_size")
-    bt = _ptr(block_tables, "block_tables", int32, dev)
-    sl = _ptr(seq_lens, "seq_lens", int32, dev)
-    T, S = key.shape[0], seq_lens.shape[0]
-    if block_tables.dim() != 2 or block_tables.shape[0] != S or seq_lens.dim() != 1:
+    bt = _ptr(block_tables, "block_tables", int32, index)
+    sl = _ptr(seq_lens, "seq_lens", int32, index)
+    T, S, tables = key.shape[0], seq_lens.shape[0], block_tables.shape
+    if len(tables) != 2 or tables[0] != S or seq_lens.dim() != 1:
         raise ValueError("block_tables must be [num_seqs, max_blocks] and seq_lens [num_seqs]")
     qs = None
     if query_start is not None:
-        qs = _ptr(query_start, "query_start", int32, dev)
+        qs = _ptr(query_start, "query_start", int32, index)
         if query_start.shape != (S + 1,):
             raise ValueError("query_start must be [num_seqs + 1]")
     elif T != S:
         raise ValueError("without query_start, key and value need a row per sequence")
-    k, k_stride = _rows(key, "key", T, Hk, D, dev)
-    v, v_stride = _rows(value, "value", T, Hk, D, dev)
-    ks, vs = _scale_ptrs(code, k_scale, v_scale, num_blocks, Hk, dev)
+    k, k_stride = _rows(key, "key", T, Hk, D, index)
+    v, v_stride = _rows(value, "value", T, Hk, D, index)
+    ks, vs = _scale_ptrs(code, k_scale, v_scale, num_blocks, Hk, index)
     table = pos = q = qo = None
     max_position = rotary_dim = Hq = q_stride = qo_stride = 0
     if cos_sin is not None:
-        table = _ptr(cos_sin, "cos_sin", (torch.float32,), dev)
+        table = _ptr(cos_sin, "cos_sin", f32, index)
         if cos_sin.dim() != 2:
             raise ValueError("cos_sin must be [max_position, rotary_dim]")
         max_position, rotary_dim = cos_sin.shape
         if positions is not None:
-            pos = _ptr(positions, "positions", int32, dev)
+            pos = _ptr(positions, "positions", int32, index)
             if positions.shape != (T,):
                 raise ValueError("positions must be [num_tokens]")
         if query is not None:
@@ -750,19 +766,24 @@ def append_kv(key_cache, value_cache, key, value, block_tables, seq_lens, block_
             if query.dim() != 3:
                 raise ValueError("query must be [num_tokens, num_heads, head_size]")
             Hq = query.shape[1]
-            q, q_stride = _rows(query, "query", T, Hq, D, dev)
-            qo, qo_stride = _rows(query_out, "query_out", T, Hq, D, dev)
+            q, q_stride = _rows(query, "query", T, Hq, D, index)
+            qo, qo_stride = _rows(query_out, "query_out", T, Hq, D, index)
         elif query_out is not None:
             raise ValueError("query_out needs query")
     elif positions is not None or query is not None or query_out is not None or interleaved:
         raise ValueError("positions, query, query_out and interleaved need cos_sin")
     o = AppendOptions(k_stride, v_stride, table, max_position, rotary_dim, bool(interleaved), Hq,
                       pos, q, qo, q_stride, qo_stride)
-    with _on_device(dev):
-        word = _status_word(dev) if status is None else status
-        rc = lib().pa_append_kv(kc, vc, k, v, T, S, Hk, D, bt, block_tables.shape[1], sl, qs, B,
-                                num_blocks, code, ks, vs,
-                                None if word is None else _ptr(word, "status", words, dev),
-                                _stream_ptr(stream, dev), ctypes.byref(o))
+    previous = _enter_device(index)
+    try:
+        if status is None:
+            word = _status_word(index)
+            word = None if word is None else word.data_ptr()
+        else:
+            word = _ptr(status, "status", (torch.int32, torch.uint32), index)
+        rc = lib().pa_append_kv(kc, vc, k, v, T, S, Hk, D, bt, tables[1], sl, qs, B, num_blocks,
+                                code, ks, vs, word, _stream_ptr(stream, index), ctypes.byref(o))
+    finally:
+        _leave_device(previous)
     _check(rc)
     return query_out
