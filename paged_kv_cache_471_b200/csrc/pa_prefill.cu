@@ -692,7 +692,7 @@ __global__ void __launch_bounds__(cta_threads(FMT == kFmtBf16), 1)
             float x[kKeys], mx = -INFINITY;
 #pragma unroll
             for (int c = 0; c < kKeys; c += 32) tmem_ld32(s_at + c, x + c);
-            tmem_wait_ld();
+            tmem_wait_ld(x);
             if (masked) {
 #pragma unroll
                 for (int c = 0; c < kKeys; ++c)
@@ -725,7 +725,7 @@ __global__ void __launch_bounds__(cta_threads(FMT == kFmtBf16), 1)
                     for (int c = 0; c < D; c += 32) {
                         float o[32];
                         tmem_ld32(o_at + c, o);
-                        tmem_wait_ld();
+                        tmem_wait_ld(o);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) o[i] *= alpha;
                         tmem_st32(o_at + c, o);
@@ -791,7 +791,7 @@ __global__ void __launch_bounds__(cta_threads(FMT == kFmtBf16), 1)
             for (int c = 0; c < D; c += 32) {
                 float o[32];
                 tmem_ld32(o_at + c, o);
-                tmem_wait_ld();
+                tmem_wait_ld(o);
                 if (any_bad && row_ok) {
                     // Non-finite values of keys that not every row of the CTA
                     // sees were left out: they make the rows that do see them

@@ -119,8 +119,13 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, float* r) {
           "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
         : "r"(addr));
 }
-__device__ __forceinline__ void tmem_wait_ld() {
+// Waits for the loads; r is what they bring, so that no use of it moves above
+// the wait.
+template <int N>
+__device__ __forceinline__ void tmem_wait_ld(float (&r)[N]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+f"(r[i]));
 }
 __device__ __forceinline__ void tmem_st32(uint32_t addr, const float* r) {
     asm volatile(
