@@ -38,12 +38,16 @@
 //
 // Counters: a generation number, the unit cursor and a count of finished
 // warps sit in the workspace header (bytes 64..75); each unit's page and
-// helper counters are 64-bit words (generation << 32 | count), so a word
-// left by an earlier call reads as zero and nothing needs clearing between
-// calls.  The last warp to finish moves the generation on and puts the
-// cursor and the count back to zero.  Every wait is bounded as in
-// pa_decode_kernel; a warp whose wait gives up drains its copies, writes
-// empty partials for the units it holds, sets PA_DEV_WAIT_TIMEOUT and stops.
+// helper counters are 64-bit words (tag of the generation << 28 | count), so
+// a word left by an earlier call reads as zero and nothing needs clearing
+// between calls.  Calls with another schedule, and prefill, put their partials
+// (fp32) and page counts (non-negative ints) over the counters: a tag begins
+// with the ten ones of a negative quiet NaN, which neither can hold (results
+// of arithmetic are 0x7fffffff when NaN).  The last warp to finish moves the
+// generation on and puts the cursor and the count back to zero.  Every wait is
+// bounded as in pa_decode_kernel; a warp whose wait gives up drains its copies,
+// writes empty partials for the units it holds, sets PA_DEV_WAIT_TIMEOUT and
+// stops.
 #pragma once
 
 #include "pa_decode_kernels.cuh"
@@ -108,20 +112,16 @@ __device__ __forceinline__ UnitRef unit_ref(const DecodeParams& p, const DynPara
     return r;
 }
 
-// Count of a generation-tagged counter word (0 when the word is from
-// another generation).
-__device__ __forceinline__ uint32_t tagged_count(unsigned long long w, uint32_t gen) {
-    return static_cast<uint32_t>(w >> 32) == gen ? static_cast<uint32_t>(w) : 0u;
-}
 
-// Add `step` to a generation-tagged counter, bringing a word left by an
+// Add `step` to a tagged counter, bringing a word left by an
 // earlier call to this generation first; returns the count before the add,
 // or 0xffffffff if the compare-and-swap never succeeded (bounded).
-__device__ __forceinline__ uint32_t tagged_add(unsigned long long* w, uint32_t gen, uint32_t step) {
+__device__ __forceinline__ uint32_t tagged_add(unsigned long long* w, unsigned long long tag,
+                                               uint32_t step) {
     unsigned long long cur = *reinterpret_cast<volatile unsigned long long*>(w);
     for (int it = 0; it < (1 << 20); ++it) {
-        const uint32_t v = tagged_count(cur, gen);
-        const unsigned long long nw = (static_cast<unsigned long long>(gen) << 32) | (v + step);
+        const uint32_t v = tagged_count(cur, tag);
+        const unsigned long long nw = tag | (v + step);
         const unsigned long long prev = atomicCAS(w, cur, nw);
         if (prev == cur) return v;
         cur = prev;
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(W * 32,
     }
     __syncwarp();
 
-    const uint32_t gen = *reinterpret_cast<volatile unsigned int*>(t.hdr);
+    const unsigned long long tag = counter_tag(*reinterpret_cast<volatile unsigned int*>(t.hdr));
     const bool cascade = p.prefix_pages > 0;
     const int rows_total = p.S * p.G;
     const size_t block_stride = static_cast<size_t>(p.Hk) * PAGE;
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(W * 32,
         nstep = claim_step(iu.n - (v + step));
         if (lane == 0) {
             const unsigned long long w = atomicAdd(t.uw + 2 * iu.u, static_cast<unsigned long long>(nstep));
-            nv = static_cast<int>(static_cast<uint32_t>(w));
+            nv = static_cast<int>(tagged_count(w, tag));
         }
         n_claimed = true;
         n_loaded = false;
@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(W * 32,
         }
         const int step = claim_step(iu.n);
         uint32_t v = 0;
-        if (lane == 0) v = tagged_add(t.uw + 2 * u, gen, static_cast<uint32_t>(step));
+        if (lane == 0) v = tagged_add(t.uw + 2 * u, tag, static_cast<uint32_t>(step));
         v = __shfl_sync(kFull, v, 0);
         if (v == 0xffffffffu) {  // the counter could not be updated: give the unit up
             if (lane == 0) atomicOr(p.status, kDevTimeout);
@@ -310,8 +310,8 @@ __global__ void __launch_bounds__(W * 32,
                 const UnitRef r = unit_ref<B>(p, t, u);
                 const volatile unsigned long long* w =
                     reinterpret_cast<volatile unsigned long long*>(t.uw + 2 * u);
-                const int used = static_cast<int>(tagged_count(w[0], gen));
-                const int helpers = static_cast<int>(tagged_count(w[1], gen));
+                const int used = static_cast<int>(tagged_count(w[0], tag));
+                const int helpers = static_cast<int>(tagged_count(w[1], tag));
                 const int left = r.n - used;
                 const int k_max = u < t.units_pre ? t.k_pre : t.k_own;
                 if (left >= 2 * t.step_min && t.owners + helpers < k_max) {
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(W * 32,
             }
             const int k_max = best_u < t.units_pre ? t.k_pre : t.k_own;
             uint32_t hs = 0;
-            if (lane == 0) hs = tagged_add(t.uw + 2 * best_u + 1, gen, 1u);
+            if (lane == 0) hs = tagged_add(t.uw + 2 * best_u + 1, tag, 1u);
             hs = __shfl_sync(kFull, hs, 0);
             if (hs == 0xffffffffu || t.owners + static_cast<int>(hs) >= k_max) continue;  // no slot
             if (join(best_u, t.owners + static_cast<int>(hs))) return true;

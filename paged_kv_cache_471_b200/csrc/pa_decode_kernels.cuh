@@ -1751,6 +1751,19 @@ __global__ void __launch_bounds__(W * 32,
     }  // segments
 }
 
+// Counter words of the dynamic schedule (pa_decode_dynamic.cuh): the tag of the
+// call's generation above a count of kDynCountBits bits.  A count is at most a
+// unit's pages (2^27) plus a claim of 64 for every warp of the grid.
+constexpr int kDynCountBits = 28;
+__device__ __forceinline__ unsigned long long counter_tag(unsigned int gen) {
+    return ((0x3ffull << 26) | (gen & 0x3ffffffu)) << kDynCountBits;
+}
+// Count of a tagged counter word (0 when the word is not of this generation).
+__device__ __forceinline__ uint32_t tagged_count(unsigned long long w, unsigned long long tag) {
+    return (w ^ tag) >> kDynCountBits ? 0u
+                                      : static_cast<uint32_t>(w) & ((1u << kDynCountBits) - 1u);
+}
+
 struct CombineParams {
     __nv_bfloat16* out;
     const float* ws_o;
@@ -1818,13 +1831,11 @@ __global__ void __launch_bounds__(kThreads) pa_combine_kernel(const CombineParam
     int br_g = 0;
     int dyn_n_pre = 0;
     if (p.dynamic) {
-        const unsigned int gen = *p.dyn_hdr - 1u;
+        const unsigned long long tag = counter_tag(*p.dyn_hdr - 1u);
         const int h = static_cast<int>(row - static_cast<long long>(s) * p.Hq);
         const int kvh = h / p.G;
         auto slots = [&](int u, int k) {
-            const unsigned long long w = p.dyn_uw[2 * u + 1];
-            const unsigned int helpers =
-                static_cast<unsigned int>(w >> 32) == gen ? static_cast<unsigned int>(w) : 0u;
+            const unsigned int helpers = tagged_count(p.dyn_uw[2 * u + 1], tag);
             return p.dyn_owners +
                    static_cast<int>(min(helpers, static_cast<unsigned int>(k - p.dyn_owners)));
         };
