@@ -535,6 +535,34 @@ pa_status pa_append_kv(void* key_cache, void* value_cache, const void* key, cons
                        int64_t num_blocks, pa_kv_dtype kv_dtype, float* k_scale, float* v_scale,
                        uint32_t* status, void* stream, const pa_append_options* opts);
 
+/* ------------------------------------------------------------------------
+ * Captured graphs.  A call that is captured into a graph uses its workspace at
+ * every replay, so that workspace belongs to the graph: two graphs that may be
+ * replayed at once, or a graph and later calls, need one each, zeroed once and
+ * kept until the graph and what was instantiated from it are gone.  These host
+ * helpers let a caller that picks workspaces for its user (as the Python
+ * binding does) find out which graph a call goes into, and how long it lives.
+ * ------------------------------------------------------------------------ */
+typedef struct pa_capture pa_capture;
+
+/* *id: the id of the capture that `stream` is in, 0 when it is in none.  Ids
+ * are not used again in a process. */
+pa_status pa_capture_id(void* stream, uint64_t* id);
+
+/* *out: a note, attached to the graph that `stream` is being captured into
+ * (PA_ERR_INVALID_ARG when it is in no capture), which pa_capture_free ends. */
+pa_status pa_capture_watch(void* stream, pa_capture** out);
+
+/* Non-zero until the graph, its copies and its executable graphs are destroyed
+ * and their launches complete. */
+int pa_capture_alive(const pa_capture* c);
+void pa_capture_free(pa_capture* c);
+
+/* Exchange the calling thread's capture mode (0 global, 1 thread local, 2
+ * relaxed; *mode receives the former one): in the relaxed mode a thread may
+ * allocate and initialise memory on other streams while it captures one. */
+pa_status pa_capture_mode(int* mode);
+
 #ifdef __cplusplus
 }
 #endif

@@ -155,6 +155,16 @@ def _bind(lib):
     lib.pa_prefill.restype = _I
     lib.pa_prefill_workspace_size.argtypes = [_I] * 8 + [ctypes.POINTER(Options)]
     lib.pa_prefill_workspace_size.restype = ctypes.c_size_t
+    lib.pa_capture_id.argtypes = [_P, ctypes.POINTER(ctypes.c_uint64)]
+    lib.pa_capture_id.restype = _I
+    lib.pa_capture_watch.argtypes = [_P, ctypes.POINTER(_P)]
+    lib.pa_capture_watch.restype = _I
+    lib.pa_capture_alive.argtypes = [_P]
+    lib.pa_capture_alive.restype = _I
+    lib.pa_capture_free.argtypes = [_P]
+    lib.pa_capture_free.restype = None
+    lib.pa_capture_mode.argtypes = [ctypes.POINTER(_I)]
+    lib.pa_capture_mode.restype = _I
     return lib
 
 
@@ -248,8 +258,11 @@ def workspace_size(num_seqs, num_heads, num_kv_heads, head_size, block_size, max
     return n
 
 
-_ws_cache = {}
+_ws_cache = {}     # (device number, stream) -> its calls' workspace
+_captured = {}     # (device number, stream, capture id) -> the _Captured of its calls
+_retired = {}      # device number -> status bits of graphs that are gone
 _status_words = {}
+_tables = threading.RLock()  # guards them
 
 
 @functools.lru_cache(maxsize=None)
@@ -267,12 +280,85 @@ def _stream_ptr(stream, index):
     return _torch()[0]._C._cuda_getCurrentRawStream(index)
 
 
-def _capturing(stream):
+def _capture_id(stream, index):
+    """The id of the capture that a call's stream is in; 0 when it is in none."""
+    if stream is None and not _torch()[0].cuda.is_current_stream_capturing():
+        return 0
+    n = ctypes.c_uint64(0)
+    _check(lib().pa_capture_id(_stream_ptr(stream, index), ctypes.byref(n)))
+    return n.value
+
+
+class _outside:
+    """``with _outside(index):`` -- torch work on device number `index` (the
+    current one) that no capture takes in, whichever streams are being captured:
+    on another stream, and complete at the end of the block."""
+
+    def __init__(self, index):
+        self.index = index
+
+    def __enter__(self):
+        torch = _torch()[0]
+        self.mode = ctypes.c_int(2)
+        _check(lib().pa_capture_mode(ctypes.byref(self.mode)))
+        try:
+            while True:  # (torch hands out a pool's streams in turn)
+                side = torch.cuda.Stream(self.index)
+                if not _capture_id(side, self.index):
+                    break
+            self.side = torch.cuda.stream(side)
+            self.side.__enter__()
+        except BaseException:
+            _check(lib().pa_capture_mode(ctypes.byref(self.mode)))
+            raise
+        self.wait = side.synchronize
+
+    def __exit__(self, *error):
+        try:
+            self.wait()
+        finally:
+            self.side.__exit__(*error)
+            _check(lib().pa_capture_mode(ctypes.byref(self.mode)))
+
+
+class _Captured:
+    """The workspaces of the calls captured into one graph on one stream.  They
+    run one after the other and share the largest; smaller ones that earlier
+    calls of the capture took stay with them."""
+
+    def __init__(self, index, stream):
+        self.index, self.buffers, self.note = index, [], ctypes.c_void_p()
+        _check(lib().pa_capture_watch(_stream_ptr(stream, index), ctypes.byref(self.note)))
+
+    def __del__(self):
+        if self.note and _lib is not None:  # (None at the end of the process)
+            _lib.pa_capture_free(self.note)
+
+    def alive(self):
+        return lib().pa_capture_alive(self.note)
+
+    def workspace(self, nbytes):
+        if not self.buffers or self.buffers[-1].numel() < nbytes:
+            torch = _torch()[0]
+            with _outside(self.index):
+                self.buffers.append(torch.zeros(nbytes, dtype=torch.uint8,
+                                                device=torch.device("cuda", self.index)))
+        return self.buffers[-1]
+
+
+def _reap(index):
+    """Let go of the workspaces of graphs of device number `index` (the current
+    one) that are gone; their status bits are kept."""
+    gone = [key for key, c in _captured.items() if c.index == index and not c.alive()]
+    if not gone:
+        return
     torch = _torch()[0]
-    if stream is None:
-        return torch.cuda.is_current_stream_capturing()
-    with torch.cuda.stream(stream):
-        return torch.cuda.is_current_stream_capturing()
+    with _outside(index):
+        if index not in _retired:
+            _retired[index] = torch.zeros(4, dtype=torch.int32, device=torch.device("cuda", index))
+        for key in gone:
+            for ws in _captured.pop(key).buffers:
+                _retired[index] |= ws[:16].view(torch.int32)
 
 
 def workspace(nbytes: int, device, stream=None):
@@ -280,28 +366,38 @@ def workspace(nbytes: int, device, stream=None):
     (default: the current one), reused by the calls on that stream (its status
     word is sticky; see read_status).  Calls on different streams may overlap,
     so each stream has its own.  While the stream is being captured into a
-    graph, the workspace is a new one that belongs to the graph alone and is
-    zeroed by each replay."""
+    graph, the workspace belongs to that graph: the calls of the capture on that
+    stream share it, nothing else does, and it is kept, status word and all,
+    until the graph is gone."""
     torch = _torch()[0]
     dev = torch.device(device)
     index = torch.cuda.current_device() if dev.index is None else dev.index
-    return _workspace(max(nbytes, WORKSPACE_HEADER_BYTES), index, stream)
+    previous = _enter_device(index)
+    try:
+        return _workspace(max(nbytes, WORKSPACE_HEADER_BYTES), index, stream)
+    finally:
+        _leave_device(previous)
 
 
 def _workspace(nbytes, index, stream):
-    """workspace for device number `index`."""
-    torch = _torch()[0]
-    capturing = _capturing(stream)
+    """workspace for device number `index`, the current one."""
+    capture = _capture_id(stream, index)
     key = (index, _stream_ptr(stream, index))
+    if capture:
+        with _tables:
+            _reap(index)
+            held = _captured.get(key + (capture,))
+            if held is None:
+                held = _captured[key + (capture,)] = _Captured(index, stream)
+            return held.workspace(nbytes)
     ws = _ws_cache.get(key)
-    if not capturing and ws is not None and ws.numel() >= nbytes:
+    if ws is not None and ws.numel() >= nbytes:
         return ws
+    torch = _torch()[0]
     if stream is None:
         stream = torch.cuda.current_stream(index)
     with torch.cuda.stream(stream):  # zeroed, and later freed, in that stream's order
         new = torch.zeros(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
-        if capturing:
-            return new
         if ws is not None:  # keep the status bits
             new[:4] = ws[:4]
     _ws_cache[key] = new
@@ -544,7 +640,7 @@ def decode_noalloc(out, query, key_cache, value_cache, num_kv_heads: int, scale:
 def read_status(workspace_tensor=None, device=None, clear=False, stream=None) -> int:
     """The sticky PA_DEV_* bits kernels set (synchronises): those of a
     workspace, or, without one, those of every call on the device that was
-    given none."""
+    given none, the replays of captured calls among them."""
     import torch
     if workspace_tensor is not None:
         dev, words = workspace_tensor.device, [workspace_tensor]
@@ -552,9 +648,16 @@ def read_status(workspace_tensor=None, device=None, clear=False, stream=None) ->
         dev = torch.device(device) if device is not None else torch.device("cuda")
         if dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
-        words = [ws for key, ws in list(_ws_cache.items()) if key[0] == dev.index]
-        if dev.index in _status_words:
-            words.append(_status_words[dev.index])
+        previous = _enter_device(dev.index)
+        try:
+            with _tables:
+                _reap(dev.index)
+                words = [ws for key, ws in list(_ws_cache.items()) if key[0] == dev.index]
+                words += [ws for c in _captured.values() if c.index == dev.index
+                          for ws in c.buffers]
+            words += [t[dev.index] for t in (_retired, _status_words) if dev.index in t]
+        finally:
+            _leave_device(previous)
         if words:  # calls of other streams may still be running
             torch.cuda.synchronize(dev)
     st = stream if stream is not None else torch.cuda.current_stream(dev)

@@ -18,7 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libpagedattn.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("pa_decode.cu", "pa_decode_block.cu", "pa_append.cu",
-                                           "pa_prefill.cu", "pa_blocks.cu")]
+                                           "pa_prefill.cu", "pa_blocks.cu", "pa_capture.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cuh")] + [
     os.path.join(INCLUDE, "pagedattn.h")]
 
