@@ -405,17 +405,21 @@ def _workspace(nbytes, index, stream):
 
 
 def _status_word(index):
-    """The device word that append_kv reports to by default; read_status reads
-    it with the workspaces'.  None while capturing if no call made it before."""
+    """The address of the device word that append_kv reports to by default;
+    read_status reads it with the workspaces'.  Made, once, for device number
+    `index` (the current one), where no capture and no stream's call sees it
+    before it is zeroed."""
     word = _status_words.get(index)
     if word is None:
         torch = _torch()[0]
-        if torch.cuda.is_current_stream_capturing():
-            return None
-        word = torch.zeros(4, dtype=torch.int32, device=torch.device("cuda", index))
-        torch.cuda.synchronize(index)  # once per device: zeroed before any stream's call
-        _status_words[index] = word
-    return word
+        with _tables:
+            word = _status_words.get(index)
+            if word is None:
+                with _outside(index):
+                    word = torch.zeros(4, dtype=torch.int32,
+                                       device=torch.device("cuda", index))
+                _status_words[index] = word
+    return word.data_ptr()
 
 
 def _enter_device(index):
@@ -881,7 +885,6 @@ def append_kv(key_cache, value_cache, key, value, block_tables, seq_lens, block_
     try:
         if status is None:
             word = _status_word(index)
-            word = None if word is None else word.data_ptr()
         else:
             word = _ptr(status, "status", (torch.int32, torch.uint32), index)
         rc = lib().pa_append_kv(kc, vc, k, v, T, S, Hk, D, bt, tables[1], sl, qs, B, num_blocks,

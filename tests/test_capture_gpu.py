@@ -2,6 +2,7 @@
 use, and for how long it is theirs."""
 
 import gc
+import threading
 import time
 
 import pytest
@@ -208,3 +209,61 @@ def test_an_abandoned_capture_keeps_nothing():
             mine |= set(pa._captured) - before
             raise RuntimeError("given up")
     assert len(mine) == 1 and let_go(mine)
+
+
+@pytest.mark.parametrize("current", [True, False])
+def test_a_first_append_in_a_capture_reports(monkeypatch, current):
+    """The first append of a process, captured on the current stream or on one
+    that is given: the capture holds, and its replays' errors are read."""
+    monkeypatch.setattr(pa, "_status_words", {})
+    s = Setup(lens=(40, 17))
+    k = queries(2, s.Hk, s.D).to(DEV)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(st):
+        graph.capture_begin()
+        if current:
+            pa.append_kv(s.kc, s.vc, k, k, s.bt, s.sl, s.B, s.kv, s.ks, s.vs)
+    if not current:
+        pa.append_kv(s.kc, s.vc, k, k, s.bt, s.sl, s.B, s.kv, s.ks, s.vs, stream=st)
+    with torch.cuda.stream(st):
+        graph.capture_end()
+    pa.read_status(device=DEV, clear=True)
+    graph.replay()
+    assert pa.read_status(device=DEV) == 0
+    s.bt[0, 2] = s.cache.num_blocks
+    graph.replay()
+    assert pa.read_status(device=DEV, clear=True) == pa.PA_DEV_BAD_BLOCK_ID
+
+
+def test_first_appends_of_two_threads_share_a_word(monkeypatch):
+    """Both threads' errors are read: each makes another one."""
+    for _ in range(20):
+        monkeypatch.setattr(pa, "_status_words", {})
+        s = Setup(lens=(40, 17), kv="bf16")
+        k = queries(2, s.Hk, s.D).to(DEV)
+        too_long = s.sl.clone()
+        too_long[0] = 1000
+        bad = s.bt.clone()
+        bad[1, 1] = -1
+        torch.cuda.synchronize()
+        gate = threading.Barrier(2)
+        failed = []
+
+        def call(tables, lens):
+            try:
+                with torch.cuda.stream(torch.cuda.Stream()):
+                    gate.wait()
+                    pa.append_kv(s.kc, s.vc, k, k, tables, lens, s.B)
+            except Exception as e:
+                failed.append(e)
+
+        threads = [threading.Thread(target=call, args=a) for a in ((s.bt, too_long), (bad, s.sl))]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        assert not failed and len(pa._status_words) == 1
+        assert pa.read_status(device=DEV, clear=True) == (pa.PA_DEV_SEQ_LEN_OUT_OF_RANGE |
+                                                          pa.PA_DEV_BAD_BLOCK_ID)
