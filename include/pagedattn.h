@@ -49,8 +49,8 @@
  * for each block and kv head (PA_KV_FP8_E4M3_BLOCK, PA_KV_INT8_BLOCK): k_scale
  * and v_scale are then fp32 arrays [num_blocks, num_kv_heads], a code c of
  * block b and kv head h standing for c * scale[b][h].  Block scales are finite
- * and not negative; when read, a V scale outside [2^-60, 2^40] counts as the
- * nearer end (below, that changes a value by at most 4e-16).
+ * and not negative, V scales at most 2^100; when read, a V scale below 2^-100
+ * counts as that (which changes a value by at most 4e-28).
  * Pointer alignment: out, query, key_cache, value_cache and workspace 16 bytes;
  * block_tables and seq_lens 4 bytes.
  * Supported shapes: head_size 64 or 128; block_size 16 or 32;

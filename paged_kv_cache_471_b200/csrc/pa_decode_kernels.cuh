@@ -151,12 +151,22 @@ enum KvCodes : int {
     kInt8Block = 2    // int8, a scale per (block, kv head)
 };
 
-// A block's V scale counts as within [2^-60, 2^40].  Within those 2^100 a
-// weight w = vs 2^(x - m) (see WarpAttn::page) of a token that matters to the
-// denominator, 2^-26 of the largest, is still a normal fp32 number, whatever
-// the other blocks' scales.  A smaller scale (a block of zeros has 2^-100, or
-// 0) changes a value by at most 448 2^-60 = 4e-16.
-constexpr float kScaleLog2Min = -60.f, kScaleLog2Max = 40.f;
+// V scales are at most 2^100, and smaller ones than 2^-100 (a block of zeros,
+// say) count as that, which changes a value by at most 448 2^-100.  While those
+// that a warp has met in a unit lie within 2^kNarrow, a weight w = vs 2^(x - m)
+// (see WarpAttn::page) of a token that matters to the denominator, 2^-26 of the
+// largest, is at least 2^(-26 - kNarrow), and the unit 2^m of a sum that matters
+// grows by less than 2^(53 + kNarrow) at once (2^27 tokens to a sum): both stay
+// normal fp32 numbers.  From then on its pages are "wide", and are handled with
+// care.
+constexpr float kScaleLog2Min = -100.f, kScaleLog2Max = 100.f;
+constexpr int kNarrow = 64;
+
+// Bounds of the V scales' base-2 logarithms met so far.
+struct ScaleRange {
+    int top = -1000, bottom = 1000;
+    __device__ __forceinline__ bool wide() const { return top - bottom > kNarrow; }
+};
 
 // The scales of the (up to two) pages of a stage: k multiplies the logits,
 // v_log2 is the base-2 logarithm of the V scale.
@@ -165,8 +175,9 @@ struct PageScales {
     float v_log2[2];
 };
 
-// One lane's scales of the pages with ids `id` and `id2` (zeros for an id
-// outside [0, num_blocks), whose page is skipped).
+// Each lane's scales of the pages with ids `id` and `id2` (none for an id
+// outside [0, num_blocks), whose page is skipped), as they are until
+// finish_page_scales: the loads' latency passes between the two.
 __device__ __forceinline__ PageScales load_page_scales(const float* k_scale, const float* v_scale,
                                                        int id, int id2, long long num_blocks,
                                                        int Hk, int kvh) {
@@ -177,10 +188,37 @@ __device__ __forceinline__ PageScales load_page_scales(const float* k_scale, con
         const bool ok = ids[i] >= 0 && static_cast<long long>(ids[i]) < num_blocks;
         const long long at = ok ? static_cast<long long>(ids[i]) * Hk + kvh : 0;
         ps.k[i] = ok ? __ldg(k_scale + at) : 0.f;
-        const float v = ok ? log2f(__ldg(v_scale + at)) : 0.f;
-        ps.v_log2[i] = fminf(fmaxf(v, kScaleLog2Min), kScaleLog2Max);
+        ps.v_log2[i] = ok ? __ldg(v_scale + at) : -1.f;  // (scales are not negative)
     }
     return ps;
+}
+
+// Logarithms of the V scales, and their range (a whole-warp call).
+__device__ __forceinline__ void finish_page_scales(PageScales& ps, ScaleRange& range) {
+    int top = range.top, bottom = range.bottom;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const bool none = ps.v_log2[i] == -1.f;
+        const float v = none ? 0.f : log2f(ps.v_log2[i]);
+        ps.v_log2[i] = fminf(fmaxf(v, kScaleLog2Min), kScaleLog2Max);
+        if (none) continue;
+        top = max(top, __float2int_ru(ps.v_log2[i]));
+        bottom = min(bottom, __float2int_rd(ps.v_log2[i]));
+    }
+    range.top = __reduce_max_sync(kFull, top);
+    range.bottom = __reduce_min_sync(kFull, bottom);
+}
+
+// The power of two to move from a row's sum l to its maximum, so that states
+// whose maxima lie far apart, because their V scales do, merge by their sums:
+// 0 unless l is outside [2^-40, 2^40] (within it, maxima of states that matter
+// to each other differ by 106 at most).
+__device__ __forceinline__ int sum_exponent(float l) {
+    if ((l >= 9.094947e-13f && l <= 1.0995116e12f) || !(l > 0.f)) return 0;
+    return min(static_cast<int>(__float_as_uint(l) >> 23) - 127, 126);
+}
+__device__ __forceinline__ float exp2_int(int e) {  // 2^e, -126 <= e <= 127
+    return __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 }
 
 // The scales that lane `src` holds.
@@ -392,6 +430,27 @@ struct WarpAttn {
         }
     }
 
+    // Block scales (after reduce_l): see sum_exponent.
+    __device__ __forceinline__ void level() {
+#pragma unroll
+        for (int r = 0; r < NH; ++r) {
+            const int e = sum_exponent(l_run[r]);
+            if (!__any_sync(kFull, e != 0)) continue;
+            const float down = exp2_int(-e);
+            l_run[r] *= down;
+            m_run[r] += static_cast<float>(e);
+            const float a0 = __shfl_sync(kFull, down, 8 * cq);
+            const float a1 = __shfl_sync(kFull, down, 8 * cq + 4);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                acc[mt][r][0] *= a0;
+                acc[mt][r][1] *= a1;
+                acc[mt][r][2] *= a0;
+                acc[mt][r][3] *= a1;
+            }
+        }
+    }
+
     // This warp's state for the CTA's merge (after reduce_l): row h of the
     // accumulator at acc_rows[h * rs + d], each row's max and sum at m16[h]
     // and l16[h] (sum 0 when zero_l).
@@ -445,8 +504,9 @@ struct WarpAttn {
                             ws_o[pr * D + 16 * mt + gq + 8 * e2] = acc[mt][hr][e1 + 2 * e2] * inv;
                 }
                 if (gq == 0) {
-                    ws_m[pr] = mh[e1];
-                    ws_l[pr] = L;
+                    const int e = BLOCK ? sum_exponent(L) : 0;
+                    ws_m[pr] = e ? mh[e1] + static_cast<float>(e) : mh[e1];
+                    ws_l[pr] = e ? L * exp2_int(-e) : L;
                 }
             }
         }
@@ -477,8 +537,12 @@ struct WarpAttn {
     // w <= 1 in f16 whatever the scales; acc sums w code.  The softmax's own
     // denominator is sum 2^(x - m) = sum w / vs, added up in fp32 from the
     // unrounded w: a page of zeros (a tiny scale) must still count there,
-    // though its w vanishes in f16.  (m, l, acc) then merge as they always do.
-    template <bool FULL, bool ALIBI>
+    // though its w vanishes in f16.  On WIDE pages (see kNarrow) w might vanish in
+    // fp32 too, and 2^(x - m) is added itself: it is at most 2^100, as m >= x +
+    // log2 vs, and at least 2^-126 where it matters, as m <= max x + 100.
+    // (m, l, acc) then merge as they always do, once a sum that is far from 1 is
+    // levelled.
+    template <bool FULL, bool ALIBI, bool WIDE = false>
     __device__ __forceinline__ void page(const uint32_t kbase, const int valid, const int valid2,
                                          const int pos0, const PageScales& window, const int src) {
         const uint32_t vbase = kbase + NPG * PAGE;
@@ -593,7 +657,8 @@ struct WarpAttn {
             const float m_new = fmaxf(m_run[r], mx);
             const float m_use = (m_new == -INFINITY) ? 0.f : m_new;
             grew |= m_new > m_run[r];
-            alpha[r] = fast_exp2(m_run[r] - m_use);
+            const float fall = m_run[r] - m_use;
+            alpha[r] = fast_exp2(fall);
             m_run[r] = m_new;
             float ls = 0.f;
 #pragma unroll
@@ -613,14 +678,22 @@ struct WarpAttn {
                     ls += bf16_lo(w) + bf16_hi(w);
                 } else {
                     w = pack_f16x2(p0, p1);
-                    if constexpr (BLOCK)
+                    if constexpr (WIDE)
+                        ls += fast_exp2(v[nt][0] - ps.v_log2[nt / (B / 8)] - m_use) +
+                              fast_exp2(v[nt][1] - ps.v_log2[nt / (B / 8)] - m_use);
+                    else if constexpr (BLOCK)
                         ls = fmaf(p0 + p1, v_inv[nt / (B / 8)], ls);
                     else
                         ls += f16_lo(w) + f16_hi(w);
                 }
                 pp[r][nt] = w;
             }
-            l_run[r] = l_run[r] * alpha[r] + ls;
+            if constexpr (WIDE) {
+                const float half = fast_exp2(0.5f * fall);  // alpha itself may vanish
+                l_run[r] = l_run[r] * half * half + ls;
+            } else {
+                l_run[r] = l_run[r] * alpha[r] + ls;
+            }
         }
 
         // ---------------- rescale O^T columns (heads 8r + 2cq, 8r + 2cq + 1),
@@ -878,7 +951,7 @@ struct WarpAttnScalar {
         }
     }
 
-    template <bool FULL, bool ALIBI>
+    template <bool FULL, bool ALIBI, bool = false>
     __device__ __forceinline__ void page(const uint32_t kbase, const int valid, const int valid2,
                                          const int pos0, const PageScales&, int) {
         const uint32_t vbase = kbase + NPG * PAGE;
@@ -1148,6 +1221,7 @@ __device__ __forceinline__ void prefix_shared_ring(const DecodeParams& p, uint32
     // Block scales: lane l holds those of stage (k & ~31) + l, loaded by every
     // warp for itself; the ids of the window after it wait in next_id.
     PageScales scales = {};
+    ScaleRange range;
     int next_id = -1, next_id2 = -1;
     if constexpr (WS::BLOCK) {
         next_id = load_win(0, 0);
@@ -1204,42 +1278,57 @@ __device__ __forceinline__ void prefix_shared_ring(const DecodeParams& p, uint32
 
     bool timed_out = false;
     int k = 0;
-    for (; k < span; ++k) {
-        const int st = k % nsh;
-        const uint32_t ph = static_cast<uint32_t>(k / nsh) & 1u;
-        if constexpr (WS::BLOCK) {
-            if ((k & 31) == 0) {
-                scales = load_page_scales(p.k_scale, p.v_scale, next_id, next_id2, p.num_blocks,
-                                          p.Hk, kvh);
-                next_id = load_win(k + 32, 0);
-                if constexpr (PAIR) next_id2 = load_win(k + 32, 1);
+    auto stream = [&](auto form) {  // as in pa_decode_kernel
+        constexpr bool WIDE = decltype(form)::value;
+        for (; k < span; ++k) {
+            const int st = k % nsh;
+            const uint32_t ph = static_cast<uint32_t>(k / nsh) & 1u;
+            if constexpr (WS::BLOCK) {
+                if ((k & 31) == 0) {
+                    scales = load_page_scales(p.k_scale, p.v_scale, next_id, next_id2,
+                                              p.num_blocks, p.Hk, kvh);
+                }
             }
-        }
-        if (!__all_sync(kFull, mbar_wait_bounded(full0 + 8 * st, ph, p.wait_limit_ns))) {
-            timed_out = true;
-            break;
-        }
-        // Prefix pages are whole blocks: every slot of a legal page is a token
-        // (a stage past the partition's last pair holds one page).
-        const uint32_t fl = lds32(flags0 + 4 * st);
-        const int valid = (fl & 1u) ? B : 0;
-        const int valid2 = (fl & 2u) ? B : 0;
-        const uint32_t kb = sbase + static_cast<uint32_t>(st * STAGE);
-        if (valid == B && (!PAIR || valid2 == B))
-            wa.template page<true, false>(kb, B, B, 0, scales, k & 31);
-        else
-            wa.template page<false, false>(kb, valid, valid2, 0, scales, k & 31);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(empty0 + 8 * st);
-        if (warp == 0 && issued < span) {
-            // Buffer st is free once every active warp has released stage k.
-            if (!__all_sync(kFull, mbar_wait_bounded(empty0 + 8 * st, ph, p.wait_limit_ns))) {
+            if (!__all_sync(kFull, mbar_wait_bounded(full0 + 8 * st, ph, p.wait_limit_ns))) {
                 timed_out = true;
-                ++k;  // stage k was consumed
-                break;
+                return;
             }
-            issue(issued++);
+            if constexpr (WS::BLOCK) {
+                if ((k & 31) == 0) {
+                    finish_page_scales(scales, range);
+                    if (!WIDE && range.wide()) return;  // (WIDE loads them again)
+                    next_id = load_win(k + 32, 0);
+                    if constexpr (PAIR) next_id2 = load_win(k + 32, 1);
+                }
+            }
+            // Prefix pages are whole blocks: every slot of a legal page is a token
+            // (a stage past the partition's last pair holds one page).
+            const uint32_t fl = lds32(flags0 + 4 * st);
+            const int valid = (fl & 1u) ? B : 0;
+            const int valid2 = (fl & 2u) ? B : 0;
+            const uint32_t kb = sbase + static_cast<uint32_t>(st * STAGE);
+            if constexpr (WIDE)
+                wa.template page<false, false, true>(kb, valid, valid2, 0, scales, k & 31);
+            else if (valid == B && (!PAIR || valid2 == B))
+                wa.template page<true, false>(kb, B, B, 0, scales, k & 31);
+            else
+                wa.template page<false, false>(kb, valid, valid2, 0, scales, k & 31);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty0 + 8 * st);
+            if (warp == 0 && issued < span) {
+                // Buffer st is free once every active warp has released stage k.
+                if (!__all_sync(kFull, mbar_wait_bounded(empty0 + 8 * st, ph, p.wait_limit_ns))) {
+                    timed_out = true;
+                    ++k;  // stage k was consumed
+                    return;
+                }
+                issue(issued++);
+            }
         }
+    };
+    stream(std::false_type{});
+    if constexpr (WS::BLOCK) {
+        if (k < span && !timed_out) stream(std::true_type{});
     }
     if (timed_out) {
         if (warp == 0) {
@@ -1632,42 +1721,64 @@ __global__ void __launch_bounds__(W * 32,
         // stage's pages, which usually takes longer).  win_a then holds those
         // stages' ids: stages up to k + NS - 1 < k + 32 have been issued.
         PageScales scales = {};
+        ScaleRange range;
         int k = 0;
-        for (; k < n_my; ++k) {
-            if constexpr (WA::BLOCK) {
-                if ((k & 31) == 0)
-                    scales = load_page_scales(p.k_scale, p.v_scale, win_a, win_a2, p.num_blocks,
-                                              p.Hk, kvh);
+        // The stages from k on, up to the first window with wide pages unless
+        // WIDE (the unusual form has a loop of its own, out of the usual one's
+        // registers).
+        auto stream = [&](auto form) {
+            constexpr bool WIDE = decltype(form)::value;
+            for (; k < n_my; ++k) {
+                if constexpr (WA::BLOCK) {
+                    if ((k & 31) == 0) {
+                        scales = load_page_scales(p.k_scale, p.v_scale, win_a, win_a2,
+                                                  p.num_blocks, p.Hk, kvh);
+                    }
+                }
+                const bool landed = mbar_wait_bounded(bar0 + 8 * stage, phase, p.wait_limit_ns);
+                if (!__all_sync(kFull, landed)) {
+                    timed_out = true;
+                    return;
+                }
+                if constexpr (WA::BLOCK) {
+                    if ((k & 31) == 0) {
+                        finish_page_scales(scales, range);
+                        if (!WIDE && range.wide()) return;  // (WIDE loads them again)
+                    }
+                }
+                const int jg = j0 + NPG * (warp + W * k);  // the stage's first logical page
+                const int valid =
+                    ((valid_mask >> (NPG * stage)) & 1u) ? min(B, T - jg * B) : 0;
+                const int valid2 = (PAIR && ((valid_mask >> (NPG * stage + 1)) & 1u))
+                                       ? min(B, T - (jg + 1) * B)
+                                       : 0;
+                const bool full = valid == B && (!PAIR || valid2 == B);
+                const uint32_t kbase = wstage0 + static_cast<uint32_t>(stage * STAGE);
+                const int pos0 = jg * B - (T - 1);  // ALiBi position of the stage's first slot
+                if constexpr (WIDE) {  // (slopes are 0 without ALiBi)
+                    wa.template page<false, true, true>(kbase, valid, valid2, pos0, scales, k & 31);
+                } else if (!has_alibi) {
+                    if (full)
+                        wa.template page<true, false>(kbase, valid, valid2, pos0, scales, k & 31);
+                    else
+                        wa.template page<false, false>(kbase, valid, valid2, pos0, scales, k & 31);
+                } else {
+                    if (full)
+                        wa.template page<true, true>(kbase, valid, valid2, pos0, scales, k & 31);
+                    else
+                        wa.template page<false, true>(kbase, valid, valid2, pos0, scales, k & 31);
+                }
+                __syncwarp();
+                if (k + NS < n_my) issue(k + NS);
+                if (++stage == NS) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
             }
-            const bool landed = mbar_wait_bounded(bar0 + 8 * stage, phase, p.wait_limit_ns);
-            if (!__all_sync(kFull, landed)) {
-                timed_out = true;
-                break;
-            }
-            const int jg = j0 + NPG * (warp + W * k);  // the stage's first logical page
-            const int valid = ((valid_mask >> (NPG * stage)) & 1u) ? min(B, T - jg * B) : 0;
-            const int valid2 =
-                (PAIR && ((valid_mask >> (NPG * stage + 1)) & 1u)) ? min(B, T - (jg + 1) * B) : 0;
-            const bool full = valid == B && (!PAIR || valid2 == B);
-            const uint32_t kbase = wstage0 + static_cast<uint32_t>(stage * STAGE);
-            const int pos0 = jg * B - (T - 1);  // ALiBi position of the stage's first slot
-            if (!has_alibi) {
-                if (full)
-                    wa.template page<true, false>(kbase, valid, valid2, pos0, scales, k & 31);
-                else
-                    wa.template page<false, false>(kbase, valid, valid2, pos0, scales, k & 31);
-            } else {
-                if (full)
-                    wa.template page<true, true>(kbase, valid, valid2, pos0, scales, k & 31);
-                else
-                    wa.template page<false, true>(kbase, valid, valid2, pos0, scales, k & 31);
-            }
-            __syncwarp();
-            if (k + NS < n_my) issue(k + NS);
-            if (++stage == NS) {
-                stage = 0;
-                phase ^= 1u;
-            }
+        };
+        stream(std::false_type{});
+        if constexpr (WA::BLOCK) {
+            if (k < n_my && !timed_out) stream(std::true_type{});
         }
 
         if (timed_out) {
@@ -1686,6 +1797,7 @@ __global__ void __launch_bounds__(W * 32,
 
         // ---------------- merge the four warps' partial softmax states
         wa.reduce_l();
+        if constexpr (WA::BLOCK) wa.level();
         __syncthreads();  // every warp is done with its stages
         float* s_acc = reinterpret_cast<float*>(smem);
         float* s_m = s_acc + W * NH * 8 * RS;

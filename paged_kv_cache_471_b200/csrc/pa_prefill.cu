@@ -130,9 +130,9 @@ struct Layout {  // shared memory, in bytes
     static constexpr int total = BF16 ? raw : raw + load_warps(BF16) * kRawBytes;
 };
 
-// Page info of a key tile: word 0, a bit per page with a legal block id; from
-// word 8, the pages' K scales; from word 16, log2 of their V scales (block
-// formats; 8 pages at most).
+// Page info of a key tile: word 0, a bit per page with a legal block id; word 1,
+// whether its pages are wide (see kNarrow); from word 8, the pages' K scales;
+// from word 16, log2 of their V scales (block formats; 8 pages at most).
 constexpr int kInfoK = 8, kInfoV = 16;
 
 constexpr float kTinyFactor = 1.17549435e-38f;  // of a logit: what is below counts as it
@@ -314,21 +314,25 @@ __global__ void __launch_bounds__(cta_threads(FMT == kFmtBf16), 1)
             }
             w = make_uint4(x[0], x[1], x[2], x[3]);
         };
+        // Block scales of a tile's pages (the first loader warp's business).
+        [[maybe_unused]] ScaleRange range;
         auto scales_of = [&](int ids) {
             PageScales ps = {};
             if constexpr (BLOCK) {
-                if (lane < NPG)
+                if (warp == kSoftmaxWarps)
                     ps = load_page_scales(p.k_scale, p.v_scale, ids, -1, p.num_blocks, p.Hk, kvh);
             }
             return ps;
         };
-        auto page_info = [&](int j, int ids, [[maybe_unused]] const PageScales& ps) {
+        auto page_info = [&](int j, int ids, [[maybe_unused]] PageScales ps) {
             // (kInfo tiles deep: the slot's last user is done once K of tile
             // j - 2 has been released.)
             float* info = reinterpret_cast<float*>(smem + L::info) + (j % kInfo) * 32;
             const unsigned legal = __ballot_sync(kFull, lane < NPG && ids >= 0);
             if (lane == 0) reinterpret_cast<uint32_t*>(info)[0] = legal;
             if constexpr (BLOCK) {
+                finish_page_scales(ps, range);
+                if (lane == 0) reinterpret_cast<uint32_t*>(info)[1] = range.wide();
                 if (lane < NPG) {
                     info[kInfoK + lane] = ps.k[0];
                     info[kInfoV + lane] = ps.v_log2[0];
@@ -674,113 +678,140 @@ __global__ void __launch_bounds__(cta_threads(FMT == kFmtBf16), 1)
         // rows' products are, they go nowhere.
         const bool idle = !__any_sync(kFull, row_ok);
         float m = -INFINITY, l = 0.f;
-        for (int j = 0; j < nt && !lost; ++j) {
-            if (!wait(s_ready + 8 * t, j)) break;
-            if (!wait(i_full + 8 * (j % kInfo), j / kInfo)) break;
-            tmem_fence_after();
-            if (idle) {
-                mbar_arrive(p_first + 8 * t);
-                mbar_arrive(p_ready + 8 * t);
-                continue;
-            }
-            const float* info = reinterpret_cast<const float*>(smem + L::info) + (j % kInfo) * 32;
-            const uint32_t legal = reinterpret_cast<const uint32_t*>(info)[0];
-            const int left = seen - (j0 + j) * kKeys;  // keys of this tile that the row sees
-            const bool masked = __any_sync(kFull, left < kKeys) || legal != (1u << NPG) - 1u;
-            // ---- the tile's scores, and their maximum (of x + log2 vs with
-            // block scales)
-            float x[kKeys], mx = -INFINITY;
-#pragma unroll
-            for (int c = 0; c < kKeys; c += 32) tmem_ld32(s_at + c, x + c);
-            tmem_wait_ld(x);
-            if (masked) {
-#pragma unroll
-                for (int c = 0; c < kKeys; ++c)
-                    if (c >= left || !((legal >> (c / B)) & 1u)) x[c] = -INFINITY;
-            }
-            if constexpr (BLOCK) {
-#pragma unroll
-                for (int pg = 0; pg < NPG; ++pg) {
-                    float y = x[pg * B];
-#pragma unroll
-                    for (int c = 1; c < B; ++c) y = fmaxf(y, x[pg * B + c]);
-                    const float f = fmaxf(mul * info[kInfoK + pg], kTinyFactor);
-                    mx = fmaxf(mx, fmaf(y, f, info[kInfoV + pg]));
+        int j = 0;
+        // The tiles from j on, up to the first wide one (see kNarrow) unless WIDE
+        // (the unusual form has a loop of its own, out of the usual one's registers).
+        auto weigh = [&](auto form) {
+            constexpr bool WIDE = decltype(form)::value;
+            for (; j < nt && !lost; ++j) {
+                if (!wait(s_ready + 8 * t, j)) break;
+                if (!wait(i_full + 8 * (j % kInfo), j / kInfo)) break;
+                tmem_fence_after();
+                if (idle) {
+                    mbar_arrive(p_first + 8 * t);
+                    mbar_arrive(p_ready + 8 * t);
+                    continue;
                 }
-            } else {
-                float y[4] = {x[0], x[1], x[2], x[3]};
+                const float* info =
+                    reinterpret_cast<const float*>(smem + L::info) + (j % kInfo) * 32;
+                const uint32_t legal = reinterpret_cast<const uint32_t*>(info)[0];
+                if (BLOCK && !WIDE && reinterpret_cast<const uint32_t*>(info)[1]) return;
+                const int left = seen - (j0 + j) * kKeys;  // keys of this tile that the row sees
+                const bool masked = __any_sync(kFull, left < kKeys) || legal != (1u << NPG) - 1u;
+                // ---- the tile's scores, and their maximum (of x + log2 vs with
+                // block scales)
+                float x[kKeys], mx = -INFINITY;
 #pragma unroll
-                for (int c = 4; c < kKeys; ++c) y[c % 4] = fmaxf(y[c % 4], x[c]);
-                mx = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) * mul;
-            }
-            // ---- O in the units of a new maximum, only when it grew by a lot
-            const bool grow = mx > m + kLazyRescale || (m == -INFINITY && mx > -INFINITY);
-            if (__any_sync(kFull, grow)) {
-                const float to = grow ? mx : m;
-                const float alpha = to == -INFINITY ? 1.f : fast_exp2(m - to);
-                m = to;
-                l *= alpha;
-                if (j > 0) {
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        float o[32];
-                        tmem_ld32(o_at + c, o);
-                        tmem_wait_ld(o);
+                for (int c = 0; c < kKeys; c += 32) tmem_ld32(s_at + c, x + c);
+                tmem_wait_ld(x);
+                if (masked) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] *= alpha;
-                        tmem_st32(o_at + c, o);
-                    }
+                    for (int c = 0; c < kKeys; ++c)
+                        if (c >= left || !((legal >> (c / B)) & 1u)) x[c] = -INFINITY;
                 }
-            }
-            const float m_use = m == -INFINITY ? 0.f : m;
-            // ---- weights back to TMEM over the scores; their sum
-            float2 sum = make_float2(0.f, 0.f);
+                if constexpr (BLOCK) {
 #pragma unroll
-            for (int c = 0; c < kKeys; c += 32) {
-                uint32_t w[16];
+                    for (int pg = 0; pg < NPG; ++pg) {
+                        float y = x[pg * B];
 #pragma unroll
-                for (int g = 0; g < 32; g += 16) {
-                    const int pg = (c + g) / B;
-                    float f = mul, add = -m_use;
-                    if constexpr (BLOCK) {
-                        f = fmaxf(mul * info[kInfoK + pg], kTinyFactor);
-                        add = info[kInfoV + pg] - m_use;
+                        for (int c = 1; c < B; ++c) y = fmaxf(y, x[pg * B + c]);
+                        const float f = fmaxf(mul * info[kInfoK + pg], kTinyFactor);
+                        mx = fmaxf(mx, fmaf(y, f, info[kInfoV + pg]));
                     }
-                    const float2 f2 = make_float2(f, f), add2 = make_float2(add, add);
-                    float2 part = make_float2(0.f, 0.f);
+                } else {
+                    float y[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
-                        const float2 y =
-                            __ffma2_rn(make_float2(x[c + g + i], x[c + g + i + 1]), f2, add2);
-                        const float2 e = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-                        part = __fadd2_rn(part, e);
-                        w[(g + i) / 2] = BF16 ? pack_bf16x2(e.x, e.y) : pack_f16x2(e.x, e.y);
-                    }
-                    if constexpr (BLOCK) {
-                        const float back = fast_exp2(-info[kInfoV + pg]);
-                        sum = __ffma2_rn(part, make_float2(back, back), sum);
+                    for (int c = 4; c < kKeys; ++c) y[c % 4] = fmaxf(y[c % 4], x[c]);
+                    mx = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) * mul;
+                }
+                // ---- O in the units of a new maximum, only when it grew by a lot
+                const bool grow = mx > m + kLazyRescale || (m == -INFINITY && mx > -INFINITY);
+                if (__any_sync(kFull, grow)) {
+                    const float to = grow ? mx : m;
+                    const float fall = to == -INFINITY ? 0.f : m - to;
+                    const float alpha = fast_exp2(fall);
+                    m = to;
+                    if constexpr (WIDE) {  // (alpha itself may vanish)
+                        const float half = fast_exp2(0.5f * fall);
+                        l = l * half * half;
                     } else {
-                        sum = __fadd2_rn(sum, part);
+                        l *= alpha;
+                    }
+                    if (j > 0) {
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            float o[32];
+                            tmem_ld32(o_at + c, o);
+                            tmem_wait_ld(o);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] *= alpha;
+                            tmem_st32(o_at + c, o);
+                        }
                     }
                 }
-                tmem_st16(s_at + c / 2, w);
-                if (c + 32 == kFirstKeys || c + 32 == kKeys) {
-                    tmem_wait_st();
-                    tmem_fence_before();
-                    mbar_arrive((c + 32 == kKeys ? p_ready : p_first) + 8 * t);
+                const float m_use = m == -INFINITY ? 0.f : m;
+                // ---- weights back to TMEM over the scores; their sum
+                float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int c = 0; c < kKeys; c += 32) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int g = 0; g < 32; g += 16) {
+                        const int pg = (c + g) / B;
+                        float f = mul, add = -m_use;
+                        if constexpr (BLOCK) {
+                            f = fmaxf(mul * info[kInfoK + pg], kTinyFactor);
+                            add = info[kInfoV + pg] - m_use;
+                        }
+                        const float2 f2 = make_float2(f, f), add2 = make_float2(add, add);
+                        [[maybe_unused]] const float2 plain2 = make_float2(-m_use, -m_use);
+                        float2 part = make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2) {
+                            const float2 y =
+                                __ffma2_rn(make_float2(x[c + g + i], x[c + g + i + 1]), f2, add2);
+                            const float2 e = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+                            if constexpr (WIDE) {  // (see WarpAttn::page)
+                                const float2 z = __ffma2_rn(
+                                    make_float2(x[c + g + i], x[c + g + i + 1]), f2, plain2);
+                                sum = __fadd2_rn(sum, make_float2(fast_exp2(z.x), fast_exp2(z.y)));
+                            } else {
+                                part = __fadd2_rn(part, e);
+                            }
+                            w[(g + i) / 2] = BF16 ? pack_bf16x2(e.x, e.y) : pack_f16x2(e.x, e.y);
+                        }
+                        if constexpr (!BLOCK) {
+                            sum = __fadd2_rn(sum, part);
+                        } else if constexpr (!WIDE) {
+                            const float back = fast_exp2(-info[kInfoV + pg]);
+                            sum = __ffma2_rn(part, make_float2(back, back), sum);
+                        }
+                    }
+                    tmem_st16(s_at + c / 2, w);
+                    if (c + 32 == kFirstKeys || c + 32 == kKeys) {
+                        tmem_wait_st();
+                        tmem_fence_before();
+                        mbar_arrive((c + 32 == kKeys ? p_ready : p_first) + 8 * t);
+                    }
                 }
+                l += sum.x + sum.y;
             }
-            l += sum.x + sum.y;
+        };
+        weigh(std::false_type{});
+        if constexpr (BLOCK) {
+            if (j < nt && !lost) weigh(std::true_type{});
         }
         // ---- the rows' results
         if (nt > 0) (void)wait(s_ready + 8 * t, nt);
         tmem_fence_after();
         const long long prow = row * p.P + part;
         const bool empty = nt == 0 || lost;
+        if (BLOCK && l == INFINITY) l = 3.4e38f;  // (rows of V scales of 2^-100: o is near 0)
         if (p.P > 1 && row_ok) {
             // (A sum of NaN goes to the merge as an overriding row of NaNs.)
-            p.ws_m[prow] = l != l ? 1e30f : m;
-            p.ws_l[prow] = empty ? 0.f : l != l ? 1.f : l;
+            const int e = BLOCK ? sum_exponent(l) : 0;
+            p.ws_m[prow] = l != l ? 1e30f : e ? m + static_cast<float>(e) : m;
+            p.ws_l[prow] = empty ? 0.f : l != l ? 1.f : e ? l * exp2_int(-e) : l;
         }
         const float inv = l > 0.f || l != l ? out_mul / l : 0.f;
         if (nt > 0 && !idle) {
