@@ -474,7 +474,8 @@ pa_status pa_copy_blocks_ex(void* key_cache, void* value_cache, float* k_scale, 
  * block_tables[s][t / block_size].  A sequence may have no rows.  Rows outside
  * [query_start[0], query_start[num_seqs]) -- padding -- are neither read nor
  * written.  query_start NULL: every sequence has one row (num_tokens ==
- * num_seqs), as in a decode step.  No two sequences of a call may append into
+ * num_seqs), as in a decode step; the row of a sequence of length 0 is padding
+ * (pa_decode gives it a zero output row).  No two sequences of a call may append into
  * the same block (copy on write sees to that).
  *
  * Rotation (opts->cos_sin): with p a token's position and R = rotary_dim, the
@@ -494,7 +495,8 @@ pa_status pa_copy_blocks_ex(void* key_cache, void* value_cache, float* k_scale, 
  * begin the block.  When a block's scale grows, the codes of its
  * earlier tokens are rounded to the new scale.  A run that begins a block
  * (t mod block_size == 0) ignores the block's old scale, so blocks need no
- * clearing when they are reused.  Infinities saturate; a NaN becomes the e4m3
+ * clearing when they are reused; elsewhere an old scale outside [2^-100, 2^100]
+ * counts as the nearer end.  Infinities saturate; a NaN becomes the e4m3
  * NaN, or int8 0.  Slots that the call's tokens do not fill keep their contents.
  *
  * Device data is checked as everywhere: a bad query_start or length skips the

@@ -815,8 +815,8 @@ def append_kv(key_cache, value_cache, key, value, block_tables, seq_lens, block_
     (views of one projection's output).  Rows query_start[s] ..
     query_start[s + 1] - 1 (int32 [num_seqs + 1]) are the last tokens of
     sequence s, whose length with them is seq_lens[s]; None: one row per
-    sequence, as in a decode step.  Rows that no sequence owns (padding) are
-    left alone.
+    sequence, as in a decode step (none for a length of 0).  Rows that no
+    sequence owns (padding) are left alone.
 
     cos_sin: fp32 [max_position, rotary_dim], a row holding the cosines, then
     the sines of its position's rotary_dim / 2 angles; pairs are (d, d +

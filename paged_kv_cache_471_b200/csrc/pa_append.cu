@@ -579,7 +579,7 @@ __device__ __forceinline__ void append_queries(const AppendParams& p, const Run&
 // f(s + 1), enough for the blocks that its n_s rows can touch (n_s / B + 2 at
 // most), so a unit finds its sequence from query_start alone, by a 32-way
 // search; units past a sequence's blocks have nothing to do.  Without
-// query_start, unit u is sequence u and its one row.
+// query_start, unit u is sequence u and its one row, if it has a length.
 template <int D, int B, int FMT, bool INTERLEAVED>
 __global__ void __launch_bounds__(kAppendWarps * 32, kAppendCtasPerSm) pa_append_kernel(const AppendParams p) {
     grid_dep_wait();
@@ -604,6 +604,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kAppendCtasPerSm) pa_append
         if (j < 0 || a == b) return;
     }
     const int T = __ldg(p.seq_lens + s);
+    if (!p.query_start && T == 0) return;  // a padded batch's row
     const int start = T - (b - a);  // the run's first index
     if (start < 0 || T > static_cast<long long>(p.max_blocks) * B) {
         if (lane == 0) flag(p, PA_DEV_SEQ_LEN_OUT_OF_RANGE);
