@@ -270,7 +270,9 @@ size_t pa_decode_workspace_size(int num_seqs, int num_heads, int num_kv_heads, i
  *  k_scale, v_scale  device pointers to one fp32 each (PA_KV_FP8_E4M3), or to
  *               fp32 [num_blocks, num_kv_heads] (block scales); required for
  *               8-bit caches, ignored for bf16.
- *  workspace    device buffer of workspace_bytes (see above).
+ *  workspace    device buffer of workspace_bytes (see above).  Calls that share
+ *               one have to follow one another: on one stream, and made by one
+ *               host thread at a time (a call may be several launches).
  *  stream       cudaStream_t to enqueue on.
  * All pointers are device pointers.  Accumulation is fp32; out is rounded
  * to bf16 (round to nearest even).

@@ -258,11 +258,15 @@ def workspace_size(num_seqs, num_heads, num_kv_heads, head_size, block_size, max
     return n
 
 
-_ws_cache = {}     # (device number, stream) -> its calls' workspace
+_ws_cache = {}     # (device number, stream) -> its calls' workspace (see _launching)
 _captured = {}     # (device number, stream, capture id) -> the _Captured of its calls
 _retired = {}      # device number -> status bits of graphs that are gone
 _status_words = {}
-_tables = threading.RLock()  # guards them
+_tables = threading.RLock()  # guards the three above
+# (device number, stream) -> held while a call finds its workspace there and
+# launches: a call may be two launches that hand partials on, and another
+# thread's call on the same stream must not come between them.
+_launching = {}
 
 
 @functools.lru_cache(maxsize=None)
@@ -374,15 +378,23 @@ def workspace(nbytes: int, device, stream=None):
     index = torch.cuda.current_device() if dev.index is None else dev.index
     previous = _enter_device(index)
     try:
-        return _workspace(max(nbytes, WORKSPACE_HEADER_BYTES), index, stream)
+        key = (index, _stream_ptr(stream, index))
+        with _launch_lock(key):
+            return _workspace(max(nbytes, WORKSPACE_HEADER_BYTES), key, stream)
     finally:
         _leave_device(previous)
 
 
-def _workspace(nbytes, index, stream):
-    """workspace for device number `index`, the current one."""
+def _launch_lock(key):
+    lock = _launching.get(key)
+    return lock if lock is not None else _launching.setdefault(key, threading.Lock())
+
+
+def _workspace(nbytes, key, stream):
+    """workspace for the key (number of the current device, its stream's pointer),
+    under the key's lock."""
+    index = key[0]
     capture = _capture_id(stream, index)
-    key = (index, _stream_ptr(stream, index))
     if capture:
         with _tables:
             _reap(index)
@@ -537,21 +549,28 @@ def decode(out, query, key_cache, value_cache, num_kv_heads: int, scale: float, 
         if alibi_slopes.shape != (Hq,):
             raise ValueError("alibi_slopes must be [num_heads]")
         alibi = _ptr(alibi_slopes, "alibi_slopes", f32, index)
+    key = (index, _stream_ptr(stream, index))
+    own = workspace_tensor is None  # (a given one is size-checked by the library)
     previous = _enter_device(index)
+    if own:
+        lock = _launch_lock(key)
+        lock.acquire()
     try:
-        if workspace_tensor is None:  # (a given one is size-checked by the library)
+        if own:
             need = _workspace_size(index, S, Hq, num_kv_heads, D, block_size, max_seq_len, code,
                                    partition_pages, num_sms, shared_prefix_blocks,
                                    bool(fp8_compute) and code == PA_KV_FP8_E4M3, schedule, stages)
-            workspace_tensor = _workspace(need, index, stream)
+            workspace_tensor = _workspace(need, key, stream)
         ws = _ptr(workspace_tensor, "workspace", None, index)
         rc = lib().pa_decode_ex(*ptrs, S, Hq, int(num_kv_heads), D, float(scale), bt, tables[1],
                                 sl, int(block_size), int(max_seq_len), num_blocks, code, ks, vs,
                                 ws, workspace_tensor.numel() * workspace_tensor.element_size(),
-                                _stream_ptr(stream, index),
+                                key[1],
                                 _opts(partition_pages, num_sms, stages, shared_prefix_blocks, alibi,
                                       fp8_compute, test_stall_copies, schedule, mha_cuda_cores))
     finally:
+        if own:
+            lock.release()
         _leave_device(previous)
     _check(rc)
     return out
@@ -596,18 +615,25 @@ def prefill(out, query, key_cache, value_cache, num_kv_heads: int, scale: float,
                          "query_start [num_seqs + 1]")
     S = tables[0]
     ks, vs = _scale_ptrs(code, k_scale, v_scale, num_blocks, num_kv_heads, index)
+    key = (index, _stream_ptr(stream, index))
+    own = workspace_tensor is None  # (a given one is size-checked by the library)
     previous = _enter_device(index)
+    if own:
+        lock = _launch_lock(key)
+        lock.acquire()
     try:
-        if workspace_tensor is None:  # (a given one is size-checked by the library)
+        if own:
             need = _prefill_workspace_size(index, T, S, Hq, num_kv_heads, D, block_size,
                                            max_seq_len, code, partition_pages, num_sms)
-            workspace_tensor = _workspace(need, index, stream)
+            workspace_tensor = _workspace(need, key, stream)
         ws = _ptr(workspace_tensor, "workspace", None, index)
         rc = lib().pa_prefill(*ptrs, T, S, Hq, int(num_kv_heads), D, float(scale), bt, tables[1],
                               sl, qs, int(block_size), int(max_seq_len), num_blocks, code, ks, vs,
                               ws, workspace_tensor.numel() * workspace_tensor.element_size(),
-                              _stream_ptr(stream, index), _opts(partition_pages, num_sms))
+                              key[1], _opts(partition_pages, num_sms))
     finally:
+        if own:
+            lock.release()
         _leave_device(previous)
     _check(rc)
     return out
