@@ -18,7 +18,7 @@ def queries(T, Hq, D, seed=2):
     return torch.randn((T, Hq, D), generator=g).to(torch.bfloat16)
 
 
-def attend(cache, q, n, scale, op="decode", **kw):
+def attend(cache, q, n, scale, op="decode", alibi=None, **kw):
     """The last n tokens of each sequence."""
     kc, vc = cache.packed(DEV)
     ks, vs = cache.scales(DEV)
@@ -28,18 +28,18 @@ def attend(cache, q, n, scale, op="decode", **kw):
     max_len = int(cache.lens.max())
     if op == "decode":
         pa.decode(out, q.to(DEV), kc, vc, cache.Hk, scale, bt, sl, cache.B, max_len, cache.kv, ks,
-                  vs, **kw)
+                  vs, alibi_slopes=None if alibi is None else alibi.to(DEV), **kw)
     else:
         pa.prefill(out, q.to(DEV), kc, vc, cache.Hk, scale, bt, sl, start.to(DEV), cache.B,
                    max_len, cache.kv, ks, vs, **kw)
     torch.cuda.synchronize()
-    ref, tol = attention(cache, q, start, scale)
+    ref, tol = attention(cache, q, start, scale, alibi)
     # kv_reference's bound counts 2^-20 A for exponentials, A = sum_t p_t |v_t|.  A
     # logit's log2 here goes with a V scale's, up to 256 in all, which fp32 rounds
     # by 2^-17 a few times: 2^-15 of every weight, in the sum and in the denominator.
     size = copy.copy(cache)
     size.v = cache.v.float().abs().to(cache.v.dtype)
-    return out.cpu().double(), ref, tol + 2.0 ** -14 * attention(size, q, start, scale)[0]
+    return out.cpu().double(), ref, tol + 2.0 ** -14 * attention(size, q, start, scale, alibi)[0]
 
 
 def check(out, ref, tol):
@@ -86,6 +86,12 @@ def test_what_append_writes_is_read(kv, op):
 LOG2 = [0, 100, -100, 60, -60, 99, -99, 30, -30, 0, -100, 100]
 
 
+def spread(cache, seed):
+    g = torch.Generator().manual_seed(seed)
+    e = torch.tensor(LOG2)[torch.randint(0, len(LOG2), (cache.num_blocks, 1), generator=g)]
+    cache.vs[:] = torch.exp2(e.double()).float()
+
+
 @pytest.mark.parametrize("kw", [dict(), dict(partition_pages=2), dict(schedule="balanced"),
                                 dict(partition_pages=5), dict(op="prefill"),
                                 dict(op="prefill", partition_pages=8)])
@@ -94,11 +100,7 @@ def test_scales_over_the_whole_range_in_one_sequence(kv, kw):
     D, B, n = 128, 16, 9 if "op" in kw else 1
     lens = [16 * 40 - 3, 16 * 9, 16 * 23 + 1]
     cache = Cache(kv, lens, 2, D, B, seed=6)
-    g = torch.Generator().manual_seed(7)
-    for s, t in enumerate(lens):
-        for j in range(-(-t // B)):
-            blk = int(cache.tables[s, j])
-            cache.vs[blk] = 2.0 ** LOG2[int(torch.randint(0, len(LOG2), (1,), generator=g))]
+    spread(cache, 7)
     q = queries(len(lens) * n, 8, D)
     check(*attend(cache, q, n, 0.125, **kw))
 
@@ -159,3 +161,28 @@ def test_a_scale_of_zero():
             cache._raw(cache.v)[blk] = 0
     for op, n in (("decode", 1), ("prefill", 20)):
         check(*attend(cache, queries(n, 4, 64), n, 0.125, op=op))
+
+
+@pytest.mark.parametrize("G", [1, 9])
+@pytest.mark.parametrize("D,B", [(128, 16), (128, 32), (64, 16), (64, 32)])
+@pytest.mark.parametrize("kv", BLOCK_FORMATS)
+def test_every_form_over_long_sequences(kv, D, B, G):
+    """More than 32 stages to a warp, one and two blocks of query rows, with and
+    without ALiBi, whole and split; prefill over many tiles."""
+    cache = Cache(kv, [9000, 33], 1, D, B, seed=11)
+    spread(cache, 12)
+    slopes = torch.linspace(0.001, 0.01, G)
+    for kw in (dict(partition_pages=9000), dict(), dict(alibi=slopes, partition_pages=9000)):
+        check(*attend(cache, queries(2, G, D), 1, 0.125, **kw))
+    for kw in (dict(partition_pages=9000), dict()):
+        check(*attend(cache, queries(6, G, D), 3, 0.125, op="prefill", **kw))
+
+
+@pytest.mark.parametrize("S,B,prefix", [(5, 16, 40), (24, 16, 300), (40, 32, 150)])
+@pytest.mark.parametrize("kv", BLOCK_FORMATS)
+def test_shared_prefix_of_a_wide_range(kv, S, B, prefix):
+    """Few sequences (a CTA per row group) and many (the shared ring)."""
+    lens = [prefix * B + (i * 29) % 200 for i in range(S)]
+    cache = Cache(kv, lens, 1, 64, B, seed=13, shared_blocks=prefix)
+    spread(cache, 14)
+    check(*attend(cache, queries(S, 4, 64), 1, 0.125, shared_prefix_blocks=prefix))
