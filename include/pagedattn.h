@@ -274,8 +274,11 @@ size_t pa_decode_workspace_size(int num_seqs, int num_heads, int num_kv_heads, i
  *               one have to follow one another: on one stream, and made by one
  *               host thread at a time (a call may be several launches).
  *  stream       cudaStream_t to enqueue on.
- * All pointers are device pointers.  Accumulation is fp32; out is rounded
- * to bf16 (round to nearest even).
+ * All pointers are device pointers.  Accumulation is fp32; the softmax weights
+ * enter their product with V in the tensor cores' operand type, bf16 for bf16
+ * caches and f16 for 8-bit ones (half a step of relative error each, 2^-8 and
+ * 2^-11; see fp8_compute and mha_cuda_cores for others); out is rounded to
+ * bf16 (round to nearest even).
  */
 pa_status pa_decode(void* out, const void* query, const void* key_cache, const void* value_cache,
                     int num_seqs, int num_heads, int num_kv_heads, int head_size, float scale,
@@ -349,9 +352,11 @@ pa_status pa_decode_noalloc(void* out, const void* query, const void* key_cache,
  *               of that many blocks, rounded up to 128 keys, at most 32 of
  *               them over max_seq_len) and num_sms; the other fields must be 0
  *               (PA_ERR_UNSUPPORTED).  By default keys are split only when the
- *               batch has too few rows for every SM.
- * Values that a row does not see have no part in it, NaNs and infinities
- * included.  The workspace holds pa_prefill_workspace_size bytes: the header
+ *               batch makes fewer than two CTAs (of 256 query rows of a kv head)
+ *               for each SM, and into as many partitions as are expected to end
+ *               soonest for sequences of max_seq_len tokens.
+ * Sums and roundings are pa_decode's.  Values that a row does not see have no
+ * part in it, NaNs and infinities included.  The workspace holds pa_prefill_workspace_size bytes: the header
  * with the status word, then, for a split call, the decode's merge counts (not
  * touched, so that one workspace serves both) and the partials.  Everything
  * else, the device-side checks and the errors, is as in pa_decode; a

@@ -30,8 +30,8 @@ constexpr int kAppendWarps = 4;
 // CTAs per SM that the kernel's registers are held to (64 a thread: 32 warps).
 // Measured on 16 prompts of 18301 tokens, 64/8 heads, bf16, and on 12271 tokens
 // in chunks, 32/8 heads, int8 blocks of 32, before the loops prefetched: 6 CTAs
-// 132 and 69 us, 8 CTAs 125 and 64, 10 CTAs (which spill) 123 and 67.  Now: 116
-// us, 6450 GB/s of rows and caches, and 57 us.
+// 132 and 69 us, 8 CTAs 125 and 64, 10 CTAs (which spill) 123 and 67.  Now:
+// 115-119 us, 6300-6500 GB/s of rows and caches, and 57-62 us.
 constexpr int kAppendCtasPerSm = 8;
 constexpr int kQueryRows = 32;  // rows of a query task (then: 16 131 us, 32 125, 64 126)
 constexpr int kStep = 16;  // slots of a V row that leave at once

@@ -29,7 +29,7 @@ using pa::kStaticSmemReserve;
 using pa::launch_decode;
 using pa::launch_pdl;
 
-constexpr int kVersion = 10100;  // 1.1.0
+constexpr int kVersion = 10200;  // 1.2.0
 constexpr size_t kSmemPerSm = 228 * 1024;
 constexpr size_t kSmemReservedPerCta = 1024;
 constexpr int kMinPartitionPages = 16;

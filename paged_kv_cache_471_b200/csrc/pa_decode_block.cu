@@ -1,10 +1,14 @@
 // The decode kernel's forms for 8-bit pages with a scale per (block, kv head).
 //
 // Bound: DRAM, as with one scale per tensor; a page's scales are 8 bytes beside
-// 4 KiB of codes.  Measured, one box (per tensor e4m3 / e4m3 blocks / int8 blocks):
-//   128 sequences of 512-8192 tokens, 64/8 heads   181 / 187 / 199 us (floor 174)
-//   32 sequences of 4096 tokens, 32/32 heads       165 / 175 / 180 us (floor 162)
-//   1 sequence of 131072 tokens, 32/8, B = 32      50.5 / 51.5 / 55.2 us (floor 41)
+// 4 KiB of codes.  Measured, one box, us on one set of inputs repeated, then on
+// three sets in turn (per tensor e4m3 / e4m3 blocks / int8 blocks):
+//   128 sequences of 512-8192 tokens, 64/8 heads (floor 174)
+//                               178 / 190 / 208     191 / 201 / 221
+//   32 sequences of 4001-4096 tokens, 32/32 heads (floor 162)
+//                               167 / 177 / 188     172 / 182 / 200
+//   1 sequence of 131072 tokens, 32/8 heads, B = 32 (floor 41)
+//                               51.4 / 51.9 / 57.8  50.3 / 51.7 / 56.5
 // The scales cost a multiply-add per logit and an exponential per page; int8
 // codes cost three more instructions per four codes than e4m3's conversion.
 #include "pa_launch.cuh"

@@ -24,10 +24,12 @@
 // clocks a step of the 256 rows.  A step takes 3500, 4000 when a row rescales: a
 // tile's chain of softmax (1980: scores loaded 240, maximum 350, weights 1390),
 // hand-overs (620) and its own products.  Measured, D = 128:
-//   1 prompt of 8192 tokens, 32/8 heads, bf16        570-620 us, 890-965 TFLOP/s
+//   1 prompt of 8192 tokens, 32/8 heads, bf16        557-632 us, 870-985 TFLOP/s
 //   4 chunks of 257-1025 tokens behind up to 4001,
-//   64/8 heads, e4m3 blocks                          352 us, 675 TFLOP/s
-// (the first at the card's power limit).  Part of the exponentials as a
+//   64/8 heads, e4m3 blocks                          355-357 us, 665-670 TFLOP/s
+// (the first at the card's power limit).  At 168 registers every form spills: 64
+// to 124 bytes of stores, 200 in the e4m3 block forms of D = 128, whose second
+// loop (see kNarrow) counts with it.  Part of the exponentials as a
 // polynomial on the FMA pipes made it slower: a quarter of them 671, half 732 us.
 #include <cuda.h>
 #include <cuda_runtime.h>
