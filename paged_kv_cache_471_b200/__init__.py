@@ -406,6 +406,8 @@ def _workspace(nbytes, key, stream):
     if ws is not None and ws.numel() >= nbytes:
         return ws
     torch = _torch()[0]
+    with _tables:
+        _reap(index)
     if stream is None:
         stream = torch.cuda.current_stream(index)
     with torch.cuda.stream(stream):  # zeroed, and later freed, in that stream's order

@@ -267,3 +267,26 @@ def test_first_appends_of_two_threads_share_a_word(monkeypatch):
         assert not failed and len(pa._status_words) == 1
         assert pa.read_status(device=DEV, clear=True) == (pa.PA_DEV_SEQ_LEN_OUT_OF_RANGE |
                                                           pa.PA_DEV_BAD_BLOCK_ID)
+
+
+def test_graphs_that_are_gone_leave_no_memory_behind():
+    """Neither by the next capture, nor by the next read of the status."""
+    s = Setup()
+    q = queries(1, s.Hq, s.D).to(DEV)
+    out = torch.empty_like(q)
+    size = 64 << 20
+    torch.cuda.synchronize()
+    before, base = set(pa._captured), torch.cuda.memory_allocated()
+
+    def fn():
+        pa.workspace(size, DEV)
+        s.decode(out, q)
+
+    for _ in range(12):
+        graph = capture(fn)
+        graph.replay()
+        mine = set(pa._captured) - before
+        del graph
+        gc.collect()
+        assert let_go(mine)
+        assert torch.cuda.memory_allocated() < base + size
